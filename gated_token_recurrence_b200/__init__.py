@@ -32,7 +32,7 @@ EXPORTED = ("gtr_gla_fwd", "gtr_gla_fwd_f16", "gtr_gla_fwd_bf16", "gtr_gla_fwd_f
             "gtr_gla_workspace_bytes", "gtr_gla_fwd_ex", "gtr_gla_fwd_host",
             "gtr_gla_read_error", "gtr_gla_plan", "gtr_gla_workspace_init", "gtr_status_string",
             "gtr_version", "gtr_gla_fwd_noalloc", "gtr_gla_block_fwd", "gtr_sswiglu_dwconv",
-            "gtr_gla_workspace_debug")
+            "gtr_gla_workspace_debug", "gtr_ssm_conv", "gtr_ssm_scan", "gtr_ssm_step", "gtr_block_norm")
 
 
 class GTRError(RuntimeError):
@@ -58,6 +58,12 @@ def _load() -> ctypes.CDLL:
     f = ctypes.c_float
     lib.gtr_gla_block_fwd.argtypes = [vp] * 7 + [i, f, vp, vp, f, vp] + [i] * 10 + [vp, sz, vp]
     lib.gtr_sswiglu_dwconv.argtypes = [vp] * 5 + [i] * 5 + [vp]
+    q = ctypes.c_int64
+    lib.gtr_ssm_conv.argtypes = [vp, q, vp, vp, vp, vp, vp, vp] + [i] * 8 + [vp]
+    ssm = [vp, q, vp, q, vp, vp, q, vp, q, vp, q, vp, vp, i, vp, vp]
+    lib.gtr_ssm_scan.argtypes = ssm + [vp, vp] + [i] * 8 + [vp]
+    lib.gtr_ssm_step.argtypes = ssm + [vp] + [i] * 5 + [vp]
+    lib.gtr_block_norm.argtypes = [vp] * 5 + [i, i, vp, f, vp, vp, i, q, i, i, i, vp]
     lib.gtr_gla_workspace_debug.argtypes = [vp, i, ctypes.c_uint, vp]
     lib.gtr_gla_workspace_bytes.argtypes = [i] * 8
     lib.gtr_gla_workspace_bytes.restype = sz
@@ -70,7 +76,8 @@ def _load() -> ctypes.CDLL:
     for name in ("gtr_gla_fwd", "gtr_gla_fwd_f16", "gtr_gla_fwd_bf16", "gtr_gla_fwd_f32",
                  "gtr_gla_fwd_ex", "gtr_gla_fwd_host", "gtr_gla_read_error", "gtr_gla_plan",
                  "gtr_gla_workspace_init", "gtr_version", "gtr_gla_fwd_noalloc", "gtr_gla_block_fwd",
-                 "gtr_sswiglu_dwconv", "gtr_gla_workspace_debug"):
+                 "gtr_sswiglu_dwconv", "gtr_gla_workspace_debug", "gtr_ssm_conv", "gtr_ssm_scan",
+                 "gtr_ssm_step", "gtr_block_norm"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -207,6 +214,173 @@ def sswiglu_dwconv(xg, xv, conv_w, conv_b, grid: Tuple[int, int], out=None, stre
                                 _dtype_code(xv), _stream_handle(stream))
     _check(st, "gtr_sswiglu_dwconv")
     return out
+
+
+def _on_current_device(what: str, *tensors):
+    import torch
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise ValueError(f"{what} takes tensors of the current CUDA device")
+
+
+def _contiguous(what: str, shape, dtype, *tensors):
+    """Tensors of one shape and type (None passes), contiguous."""
+    for t in tensors:
+        if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()):
+            raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                             f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _rows(what: str, t, shape, dtype, tokens: int) -> int:
+    """The distance between the rows of consecutive tokens of a tensor whose first `tokens`
+    axes are batch and token axes; a row itself is contiguous."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    width = 1
+    for size, stride in zip(reversed(t.shape[tokens:]), reversed(t.stride()[tokens:])):
+        if size != 1 and stride != width:
+            raise ValueError(f"{what}: the values of one token must be contiguous")
+        width *= size
+    ld, behind = None, 1  # rows from one index of an axis to the next
+    for size, stride in zip(reversed(t.shape[:tokens]), reversed(t.stride()[:tokens])):
+        if size != 1:
+            if ld is None:
+                ld = stride // behind
+            if stride != ld * behind:
+                raise ValueError(f"{what}: consecutive tokens must be evenly spaced")
+        behind *= size
+    if ld is None:  # one token in all: any valid distance
+        unit = 16 // t.element_size()
+        ld = -(-width // unit) * unit
+    return ld
+
+
+def _grid_tokens(t, grid):
+    H, W = grid
+    if t.shape[1] != H * W:
+        raise ValueError(f"grid {H}x{W} does not match L={t.shape[1]}")
+    return int(H), int(W)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def ssm_conv(x, w, bias, grid: Tuple[int, int], direction: int = L2R, silu: bool = True, state=None,
+             state_out=None, lengths=None, out=None, stream=None):
+    """Short causal depthwise convolution along the scan (``gtr_ssm_conv``); returns ``out``.
+
+    ``x`` [B, L, C] (L = H * W; may be a column range of wider rows), ``w`` [C, K] fp32 with
+    K = 2, 3 or 4, ``bias`` [C] fp32 or None.  ``state`` [B, K-1, C] holds the inputs before the
+    first token (None: zeros); the last K-1 inputs are written to ``state_out``, which may be
+    ``state``.  For a single new token per sequence the grid is (1, 1).  ``lengths`` [B] int32:
+    tokens of each sequence of a padded batch; outputs behind them are left as they were.
+    """
+    import torch
+    B, L, C = x.shape
+    H, W = _grid_tokens(x, grid)
+    K = int(w.shape[-1])
+    if out is None:
+        out = torch.empty((B, L, C), dtype=x.dtype, device=x.device)
+    _on_current_device("ssm_conv", x, w, bias, state, state_out, lengths, out)
+    ld = _rows("ssm_conv x", x, (B, L, C), x.dtype, 2)
+    _contiguous("ssm_conv w", (C, K), torch.float32, w)
+    _contiguous("ssm_conv bias", (C,), torch.float32, bias)
+    _contiguous("ssm_conv state", (B, K - 1, C), x.dtype, state, state_out)
+    _contiguous("ssm_conv lengths", (B,), torch.int32, lengths)
+    _contiguous("ssm_conv out", (B, L, C), x.dtype, out)
+    _check(lib.gtr_ssm_conv(x.data_ptr(), ld, w.data_ptr(), _ptr(bias), _ptr(state), _ptr(state_out), _ptr(lengths),
+                            out.data_ptr(), B, H, W, C, K, int(direction), int(silu), _dtype_code(x),
+                            _stream_handle(stream)), "gtr_ssm_conv")
+    return out
+
+
+def _ssm_inputs(what, u, dt, A, Bm, Cm, z, skip, dt_bias, state, state_out, lead):
+    """The arguments that a scan and a step share; ``lead`` is (B, L) or (B,)."""
+    import torch
+    D, N = A.shape
+    G = int(Bm.shape[-2])
+    _on_current_device(what, u, dt, A, Bm, Cm, z, skip, dt_bias, state, state_out)
+    k = len(lead)
+    ld = lambda name, t, tail: _rows(f"{what} {name}", t, (*lead, *tail), u.dtype, k)
+    _contiguous(f"{what} A", (D, N), torch.float32, A)
+    _contiguous(f"{what} skip, dt_bias", (D,), torch.float32, skip, dt_bias)
+    _contiguous(f"{what} state", (lead[0], D, N), torch.float32, state, state_out)
+    return ([u.data_ptr(), ld("u", u, (D,)), dt.data_ptr(), ld("dt", dt, (D,)), A.data_ptr(), Bm.data_ptr(),
+             ld("Bm", Bm, (G, N)), Cm.data_ptr(), ld("Cm", Cm, (G, N)), _ptr(z),
+             0 if z is None else ld("z", z, (D,)), _ptr(skip), _ptr(dt_bias)], D, N, G)
+
+
+def ssm_scan(u, dt, A, Bm, Cm, grid: Tuple[int, int], direction: int = L2R, skip=None, z=None, dt_bias=None,
+             softplus: bool = True, state=None, state_out=None, lengths=None, out=None, stream=None):
+    """Selective state space scan over a prompt (``gtr_ssm_scan``); returns ``out`` [B, L, D].
+
+    ``u``, ``dt`` and the optional gate ``z`` [B, L, D], ``Bm`` and ``Cm`` [B, L, G, N] (each may
+    be a column range of wider rows), ``A`` [D, N], ``skip`` and ``dt_bias`` [D] fp32.  ``state``
+    [B, D, N] fp32 is h before the first token (None: zeros); h after the last is written to
+    ``state_out``, which may be ``state``.  ``lengths`` as for :func:`ssm_conv`.
+    """
+    import torch
+    B, L, D = u.shape
+    H, W = _grid_tokens(u, grid)
+    if out is None:
+        out = torch.empty((B, L, D), dtype=u.dtype, device=u.device)
+    args, D, N, G = _ssm_inputs("ssm_scan", u, dt, A, Bm, Cm, z, skip, dt_bias, state, state_out, (B, L))
+    _on_current_device("ssm_scan", lengths, out)
+    _contiguous("ssm_scan lengths", (B,), torch.int32, lengths)
+    _contiguous("ssm_scan out", (B, L, D), u.dtype, out)
+    _check(lib.gtr_ssm_scan(*args, int(softplus), _ptr(state), _ptr(state_out), _ptr(lengths), out.data_ptr(), B, H, W,
+                            D, N, G, int(direction), _dtype_code(u), _stream_handle(stream)), "gtr_ssm_scan")
+    return out
+
+
+def ssm_step(u, dt, A, Bm, Cm, state, skip=None, z=None, dt_bias=None, softplus: bool = True, state_out=None,
+             out=None, stream=None):
+    """Selective scan of one new token per sequence (``gtr_ssm_step``); returns ``out`` [B, D].
+
+    ``u``, ``dt``, ``z`` [B, D], ``Bm`` and ``Cm`` [B, G, N]; the states ``state`` [B, D, N] fp32 are
+    updated in place, or written to ``state_out`` where it is given.
+    """
+    import torch
+    B, D = u.shape
+    state_out = state if state_out is None else state_out
+    if out is None:
+        out = torch.empty((B, D), dtype=u.dtype, device=u.device)
+    args, D, N, G = _ssm_inputs("ssm_step", u, dt, A, Bm, Cm, z, skip, dt_bias, state, state_out, (B,))
+    _on_current_device("ssm_step", out)
+    _contiguous("ssm_step out", (B, D), u.dtype, out)
+    _check(lib.gtr_ssm_step(*args, int(softplus), state.data_ptr(), state_out.data_ptr(), out.data_ptr(), B, D, N, G,
+                            _dtype_code(u), _stream_handle(stream)), "gtr_ssm_step")
+    return out
+
+
+def block_norm(y, h, post_w=None, pre_w=None, gate=None, gate_silu: bool = False, scale=None, eps: float = 1e-6,
+               h_out=None, n_out=None, stream=None):
+    """The norms around a block with its gate, residual scale and residual stream (``gtr_block_norm``).
+
+    h' = h + scale * act(gate) * RMSNorm(y) * post_w and n = RMSNorm(h') * pre_w; returns (h', n),
+    n None without ``pre_w``.  ``y`` [B, L, C]; ``h`` [B, L, C] of the same type or fp32; ``gate``
+    [B, C] or [B, L, C]; ``post_w``, ``pre_w``, ``scale`` [C] fp32.  ``h_out`` may be ``h`` and ``n_out``
+    may be ``y``.
+    """
+    import torch
+    B, L, C = y.shape
+    if h_out is None:
+        h_out = torch.empty_like(h)
+    if n_out is None and pre_w is not None:
+        n_out = torch.empty_like(y)
+    if pre_w is None and n_out is not None:
+        raise ValueError("block_norm: n_out without pre_w")
+    _on_current_device("block_norm", y, h, post_w, pre_w, gate, scale, h_out, n_out)
+    per_token = gate is not None and gate.dim() == 3
+    _contiguous("block_norm y, n_out", (B, L, C), y.dtype, y, n_out)
+    _contiguous("block_norm h, h_out", (B, L, C), h.dtype, h, h_out)
+    _contiguous("block_norm gate", (B, L, C) if per_token else (B, C), y.dtype, gate)
+    _contiguous("block_norm post_w, pre_w, scale", (C,), torch.float32, post_w, pre_w, scale)
+    _check(lib.gtr_block_norm(y.data_ptr(), h.data_ptr(), _ptr(post_w), _ptr(pre_w), _ptr(gate), int(per_token),
+                              int(gate_silu), _ptr(scale), float(eps), h_out.data_ptr(), _ptr(n_out), B, L, C,
+                              _dtype_code(y), _dtype_code(h), _stream_handle(stream)), "gtr_block_norm")
+    return h_out, n_out
 
 
 def gla_fwd_host(q, k, v, log_gamma, out, grid: Tuple[int, int], direction: int = L2R,

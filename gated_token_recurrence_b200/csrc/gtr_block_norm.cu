@@ -1,0 +1,203 @@
+// The norms around a block, fused with the block's gate, its residual scale and the residual
+// stream.  Per token row (C channels), y the block's output and h the residual stream:
+//
+//     p  = y / sqrt(mean_c y^2 + eps) * post_w        (no post_w: p = y)
+//     h' = h + scale * act(gate) * p                  (no scale, no gate: factor 1)
+//     n  = h' / sqrt(mean_c h'^2 + eps) * pre_w       (from h' before its rounding)
+//
+// One pass over the data: a row is held in the registers of TPR threads (a warp for rows of
+// up to 64 pieces of 16 bytes, a CTA above), the two sums of squares are reduced in fp32 with
+// shuffles, and h' never returns from memory for its norm.  Bound by HBM bandwidth: y, h and
+// the gate are read once, h' and n written once.
+#include "gtr_common.cuh"
+#include "gtr_launch.cuh"
+#include "gtr_vec.cuh"
+
+namespace gtr {
+namespace {
+
+struct NormParams {
+  const void* y;
+  const void* h;
+  const float* post_w;  // [C] or nullptr
+  const float* pre_w;   // [C] or nullptr (then n is not written)
+  const void* gate;     // [B][C] or [B][L][C] or nullptr
+  const float* scale;   // [C] or nullptr
+  void* h_out;
+  void* n_out;
+  float eps;
+  long long rows;
+  int L, C, gate_rows, silu;  // gate_rows: 0 none, 1 per sequence, 2 per token
+};
+
+// N consecutive values of T as fp32, N a multiple of 16 / sizeof(T)
+template <typename T, int N>
+__device__ __forceinline__ void load_row(const T* p, float* f) {
+#pragma unroll
+  for (int i = 0; i < N; i += Vec8<T>::N) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p + i);
+    Vec8<T>::load(u, f + i);
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* p, const float* f) {
+#pragma unroll
+  for (int i = 0; i < N; i += Vec8<T>::N) *reinterpret_cast<uint4*>(p + i) = Vec8<T>::store(f + i);
+}
+
+// Sum over the row's TPR threads, the same value in each of them.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (TPR > 32) {
+    __syncthreads();  // the previous sum has been read
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) v += red[i];
+  }
+  return v;
+}
+
+// T: y, gate and n; R: the residual stream; NV pieces of 16 / sizeof(T) channels a thread.
+template <typename T, typename R, int TPR, int NV>
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128) block_norm_kernel(const NormParams p) {
+  constexpr int kN = Vec8<T>::N;
+  constexpr int kRowsPerCta = TPR >= 128 ? 1 : 128 / TPR;
+  __shared__ float red[TPR / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x % TPR;
+  const long long row = (long long)blockIdx.x * kRowsPerCta + threadIdx.x / TPR;
+  if (row >= p.rows) return;  // whole rows' threads at once: they are whole warps, or the CTA
+  const int nvec = p.C / kN;
+  const T* y = static_cast<const T*>(p.y) + row * p.C;
+  const R* h = static_cast<const R*>(p.h) + row * p.C;
+  float fy[NV][kN], fh[NV][kN];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TPR + lane) * kN;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) fy[v][e] = fh[v][e] = 0.f;
+    if (v * TPR + lane < nvec) {
+      load_row<T, kN>(y + c, fy[v]);
+      load_row<R, kN>(h + c, fh[v]);
+    }
+  }
+  float rp = 1.f;
+  if (p.post_w) {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < kN; ++e) s = fmaf(fy[v][e], fy[v][e], s);
+    rp = rsqrtf(row_sum<TPR>(s, red) / (float)p.C + p.eps);
+  }
+  const T* gate = static_cast<const T*>(p.gate) + (p.gate_rows == 1 ? row / p.L : row) * p.C;
+  float s2 = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TPR + lane) * kN;
+    if (v * TPR + lane < nvec) {
+      float f[kN];
+      if (p.post_w) {
+        load_row<float, kN>(p.post_w + c, f);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) fy[v][e] *= rp * f[e];
+      }
+      if (p.gate_rows) {
+        load_row<T, kN>(gate + c, f);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) fy[v][e] *= p.silu ? __fdividef(f[e], 1.f + __expf(-f[e])) : f[e];
+      }
+      if (p.scale) {
+        load_row<float, kN>(p.scale + c, f);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) fy[v][e] *= f[e];
+      }
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        fh[v][e] += fy[v][e];
+        s2 = fmaf(fh[v][e], fh[v][e], s2);
+      }
+      store_row<R, kN>(static_cast<R*>(p.h_out) + row * p.C + c, fh[v]);
+    }
+  }
+  if (!p.pre_w) return;
+  const float rn = rsqrtf(row_sum<TPR>(s2, red) / (float)p.C + p.eps);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TPR + lane) * kN;
+    if (v * TPR + lane < nvec) {
+      float f[kN];
+      load_row<float, kN>(p.pre_w + c, f);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) f[e] *= rn * fh[v][e];
+      store_row<T, kN>(static_cast<T*>(p.n_out) + row * p.C + c, f);
+    }
+  }
+}
+
+template <typename T, typename R, int TPR, int NV>
+gtr_status_t launch_norm(const NormParams& p, cudaStream_t stream) {
+  constexpr int kRowsPerCta = TPR >= 128 ? 1 : 128 / TPR;
+  const long long grid = (p.rows + kRowsPerCta - 1) / kRowsPerCta;
+  if (grid > 0x7fffffffll) return GTR_ERR_UNSUPPORTED;
+  return launch_serial(block_norm_kernel<T, R, TPR, NV>, dim3((unsigned)grid), dim3(TPR > 128 ? TPR : 128), 0, stream, p);
+}
+
+template <typename T, typename R>
+gtr_status_t launch_norm_c(const NormParams& p, cudaStream_t stream) {
+  const int nvec = p.C / Vec8<T>::N;
+  if (nvec <= 32) return launch_norm<T, R, 32, 1>(p, stream);
+  if (nvec <= 64) return launch_norm<T, R, 32, 2>(p, stream);
+  if (nvec <= 128) return launch_norm<T, R, 128, 1>(p, stream);
+  if (nvec <= 256) return launch_norm<T, R, 128, 2>(p, stream);
+  if (nvec <= 512) return launch_norm<T, R, 256, 2>(p, stream);
+  if (nvec <= 1024) return launch_norm<T, R, 512, 2>(p, stream);
+  if (nvec <= 2048) return launch_norm<T, R, 512, 4>(p, stream);
+  return GTR_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+}  // namespace gtr
+
+extern "C" gtr_status_t gtr_block_norm(const void* y, const void* h, const float* post_w, const float* pre_w,
+                                       const void* gate, int gate_per_token, int gate_silu, const float* scale,
+                                       float eps, void* h_out, void* n_out, int B, int64_t L, int C, int dtype,
+                                       int residual_dtype, gtr_stream_t stream) {
+  using namespace gtr;
+  if (!y || !h || !h_out || (pre_w != nullptr) != (n_out != nullptr) || B <= 0 || L <= 0 || C <= 0)
+    return GTR_ERR_INVALID_ARG;
+  if (dtype < GTR_F32 || dtype > GTR_BF16 || residual_dtype < GTR_F32 || residual_dtype > GTR_BF16)
+    return GTR_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || eps > 3.4e38f) return GTR_ERR_INVALID_ARG;
+  for (const void* q : {y, h, (const void*)post_w, (const void*)pre_w, gate, (const void*)scale, (const void*)h_out,
+                        (const void*)n_out})
+    if (!aligned_to(q, 16)) return GTR_ERR_INVALID_ARG;
+  if (residual_dtype != dtype && residual_dtype != GTR_F32) return GTR_ERR_UNSUPPORTED;
+  const int es = dtype == GTR_F32 ? 4 : 2, er = residual_dtype == GTR_F32 ? 4 : 2;
+  if (C % (16 / es) != 0 || C > 2048 * (16 / es)) return GTR_ERR_UNSUPPORTED;
+  if (L > (1ll << 28) || (double)B * L * C >= 1e12) return GTR_ERR_UNSUPPORTED;
+  const long long rows = (long long)B * L;
+  const size_t ny = (size_t)rows * C * es, nh = (size_t)rows * C * er, nw = (size_t)C * 4;
+  const size_t ng = (size_t)(gate_per_token ? rows : B) * C * es;
+  if ((h_out != h && overlaps(h_out, nh, h, nh)) || overlaps(h_out, nh, y, ny) || overlaps(h_out, nh, gate, ng) ||
+      overlaps(h_out, nh, n_out, ny) || overlaps(n_out, ny, h, nh) || (n_out != y && overlaps(n_out, ny, y, ny)) ||
+      overlaps(n_out, ny, gate, ng))
+    return GTR_ERR_INVALID_ARG;
+  for (const void* q : {post_w, pre_w, scale})
+    if (overlaps(h_out, nh, q, nw) || overlaps(n_out, ny, q, nw)) return GTR_ERR_INVALID_ARG;
+  NormParams p{y, h, post_w, pre_w, gate, scale, h_out, n_out, eps, rows, (int)L, C,
+               gate ? (gate_per_token ? 2 : 1) : 0, gate_silu != 0};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool wide = residual_dtype == GTR_F32;
+  switch (dtype) {
+    case GTR_F16: return wide ? launch_norm_c<__half, float>(p, s) : launch_norm_c<__half, __half>(p, s);
+    case GTR_BF16:
+      return wide ? launch_norm_c<__nv_bfloat16, float>(p, s) : launch_norm_c<__nv_bfloat16, __nv_bfloat16>(p, s);
+    default: return launch_norm_c<float, float>(p, s);
+  }
+}

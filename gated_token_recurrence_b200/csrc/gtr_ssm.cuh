@@ -1,0 +1,62 @@
+// What the selective scan's kernels share: the problem and the per-token scalar functions.
+#pragma once
+
+#include "gtr_common.cuh"
+#include "gtr_scan_order.cuh"
+
+namespace gtr {
+
+// Per (sequence b, channel d), with s the position in the scan order and N states:
+//     delta_s  = softplus(dt_s + dt_bias_d)                    (or dt_s + dt_bias_d)
+//     h_s[n]   = exp(delta_s A_d[n]) h_{s-1}[n] + delta_s u_s B_s[n]
+//     out_s    = ( sum_n C_s[n] h_s[n] + skip_d u_s ) SiLU(z_s)
+struct SsmParams {
+  const void* u;
+  const void* dt;
+  const void* Bm;  // rows [G][N]
+  const void* Cm;
+  const void* z;  // or nullptr
+  long long u_ld, dt_ld, bm_ld, cm_ld, z_ld;  // elements between tokens
+  const float* A;         // [D][N]
+  const float* skip;      // [D] or nullptr
+  const float* dt_bias;   // [D] or nullptr
+  const float* state_in;  // [B][D][N] or nullptr
+  float* state_out;       // [B][D][N] or nullptr; may be state_in
+  const int* lengths;     // [B] or nullptr
+  void* out;              // [B][L][D]
+  int B, L, D, N, G, softplus;
+  ScanMap map;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// log(1 + exp(x)) = max(x, 0) + log1p(e) with e = exp(-|x|) in (0, 1].  Steps are small (a
+// thousandth is common), so the relative error matters: the exponential carries the rounding
+// of its argument as a first-order correction, and log1p(e) = 2 atanh(s), s = e / (2 + e) <=
+// 1/3, by its odd series; the first term left out is 2 s^15 / 15 <= 1e-8 of the sum.
+__device__ __forceinline__ float softplus_f32(float x) {
+  const float a = fmaxf(-fabsf(x), -100.f);  // e^-100 is 0 in fp32; an infinite x stays out of the products
+  const float hi = a * kLog2e;
+  const float lo = fmaf(a, kLog2e, -hi) + a * 1.925963033500e-8f;  // log2(e) = kLog2e + 1.9259...e-8
+  const float e0 = exp2_approx(hi);
+  const float e = fmaf(e0, lo * 0.69314718f, e0);
+  const float s = __fdividef(e, 2.f + e);
+  const float q = s * s;
+  float t = 1.f / 13.f;
+  t = fmaf(t, q, 1.f / 11.f);
+  t = fmaf(t, q, 1.f / 9.f);
+  t = fmaf(t, q, 1.f / 7.f);
+  t = fmaf(t, q, 1.f / 5.f);
+  t = fmaf(t, q, 1.f / 3.f);
+  return (x < 0.f ? 0.f : x) + 2.f * fmaf(s * q, t, s);  // a NaN stays one
+}
+
+__device__ __forceinline__ float ssm_silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+
+}  // namespace gtr

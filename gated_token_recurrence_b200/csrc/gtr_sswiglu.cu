@@ -24,6 +24,7 @@
 
 #include "gtr_common.cuh"
 #include "gtr_sm100.cuh"
+#include "gtr_vec.cuh"
 
 namespace gtr {
 namespace {
@@ -44,57 +45,6 @@ struct alignas(64) SwParams {
   const float* b;  // [C] or nullptr
   int B, H, W, C;
   int tiles_x, tiles_y, cblocks;
-};
-
-template <typename T> struct Vec8;  // 16 bytes of T <-> fp32
-template <> struct Vec8<__half> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const uint4& u, float* f) {
-    const __half2* h = reinterpret_cast<const __half2*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = __half22float2(h[i]);
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
-  }
-  static __device__ __forceinline__ uint4 store(const float* f) {
-    uint4 u;
-    __half2* h = reinterpret_cast<__half2*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-    return u;
-  }
-};
-template <> struct Vec8<__nv_bfloat16> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const uint4& u, float* f) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ uint4 store(const float* f) {
-    uint4 u;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    return u;
-  }
-};
-template <> struct Vec8<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ void load(const uint4& u, float* f) {
-    f[0] = __uint_as_float(u.x);
-    f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z);
-    f[3] = __uint_as_float(u.w);
-  }
-  static __device__ __forceinline__ uint4 store(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
 };
 
 template <typename T>

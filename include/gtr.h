@@ -278,6 +278,102 @@ gtr_status_t gtr_sswiglu_dwconv(const void *xg, const void *xv, const float *con
                                 gtr_stream_t stream);
 
 /*
+ * The operators below are the pieces of a block whose token mixer is a selective state
+ * space model instead of (or next to) key-only GLA, and of the residual stream around any
+ * block; the pages of the GTR paper have no counterpart.  Like the rest of the library they
+ * are forward only.  Rules that they share:
+ *
+ *   - all pointers are device pointers of the current device; data pointers are 16-byte
+ *     aligned, pointers to per-channel vectors and lengths 4-byte (gtr_block_norm: 16);
+ *   - asynchronous on `stream`, no workspace, no allocation, no synchronisation; capturable;
+ *     calls on different streams and captured graphs are independent of one another;
+ *   - `*_ld` is the distance, in elements, between the rows of consecutive tokens m (and of
+ *     the last token of a sequence and the first of the next), a multiple of 16 bytes: an
+ *     input may be a column range of a wider projection.  Outputs are contiguous;
+ *   - no output may overlap an input or another output, except where an argument says that
+ *     it may be the same buffer (GTR_ERR_INVALID_ARG);
+ *   - sums, states and norms are held in fp32; each output is rounded once;
+ *   - `direction` is the scan order of gtr_gla_fwd over grid_H x grid_W tokens per sequence.
+ *     A plain sequence of L tokens is the grid 1 x L in direction GTR_L2R;
+ *   - `lengths` [B] int32 (or NULL: all full) gives the number of tokens that each sequence of
+ *     a padded batch has: its first lengths[b] positions in scan order.  Values outside
+ *     0 .. L are taken as the nearest of the two.  Inputs behind a sequence's end are not
+ *     read into any result, outputs behind it are left as they were, and carried states are
+ *     those after lengths[b] tokens (for length 0: the states that came in).
+ */
+
+/*
+ * Short causal depthwise convolution along the scan, the step in front of a selective scan:
+ *     out_s[c] = act( bias[c] + sum_{k < K} w[c, k] x_{s - K + 1 + k}[c] )
+ * with s the position in scan order (the state of the convolution carries across line ends)
+ * and act = SiLU where `silu` is not 0, else the identity.  Prompts and single tokens alike:
+ * for one new token per sequence the grid is 1 x 1 and state_in = state_out is its cache.
+ *   x [B, L, C] rows x_ld apart, out [B, L, C], in `dtype`
+ *   w [C, K] fp32, K = 2, 3 or 4 (otherwise GTR_ERR_UNSUPPORTED);  bias [C] fp32 or NULL
+ *   state_in [B, K-1, C] in `dtype`: the inputs of the K-1 positions before the first, oldest
+ *     first (NULL: zeros);  state_out, the same layout: the last K-1 inputs (NULL: not
+ *     wanted; may be state_in)
+ *   C a multiple of 8 (16-bit data) or 4 (fp32), otherwise GTR_ERR_UNSUPPORTED.
+ */
+gtr_status_t gtr_ssm_conv(const void *x, int64_t x_ld, const float *w, const float *bias,
+                          const void *state_in, void *state_out, const int *lengths, void *out,
+                          int B, int grid_H, int grid_W, int C, int K, int direction, int silu,
+                          int dtype, gtr_stream_t stream);
+
+/*
+ * Selective state space scan over a prompt.  Per (sequence b, channel d) with N states, g the
+ * channel's group (d / (D / G)) and s the position in scan order:
+ *     delta_s = softplus(dt_s[d] + dt_bias[d])        (softplus = 0: dt_s[d] + dt_bias[d])
+ *     h_s[n]  = exp(delta_s A[d, n]) h_{s-1}[n] + delta_s u_s[d] Bm_s[g, n]
+ *     out_s   = ( sum_n Cm_s[g, n] h_s[n] + skip[d] u_s[d] ) SiLU(z_s[d])
+ *   u, dt, z [B, L, D] rows u_ld, dt_ld, z_ld apart, out [B, L, D], in `dtype`; z NULL: no gate
+ *   Bm, Cm [B, L, G, N] in `dtype`, rows bm_ld, cm_ld apart (the G * N values of a token
+ *     contiguous)
+ *   A [D, N] fp32, delta * A <= 0 (not checked);  skip, dt_bias [D] fp32 or NULL (0)
+ *   state_in [B, D, N] fp32: h before the first position (NULL: zeros);  state_out: h after
+ *     the last (NULL: not wanted; may be state_in)
+ *   N a multiple of 8 up to 64;  D / G a multiple of 16;  B <= 65535; otherwise
+ *   GTR_ERR_UNSUPPORTED.
+ */
+gtr_status_t gtr_ssm_scan(const void *u, int64_t u_ld, const void *dt, int64_t dt_ld, const float *A,
+                          const void *Bm, int64_t bm_ld, const void *Cm, int64_t cm_ld,
+                          const void *z, int64_t z_ld, const float *skip, const float *dt_bias,
+                          int softplus, const float *state_in, float *state_out, const int *lengths,
+                          void *out, int B, int grid_H, int grid_W, int D, int N, int G,
+                          int direction, int dtype, gtr_stream_t stream);
+
+/*
+ * The same for one new token per sequence: u, dt, z, out [B, D], Bm, Cm [B, G, N], the `*_ld`
+ * between the rows of consecutive sequences; state_in and state_out [B, D, N] fp32 are both
+ * required and may be the same buffer.
+ */
+gtr_status_t gtr_ssm_step(const void *u, int64_t u_ld, const void *dt, int64_t dt_ld, const float *A,
+                          const void *Bm, int64_t bm_ld, const void *Cm, int64_t cm_ld,
+                          const void *z, int64_t z_ld, const float *skip, const float *dt_bias,
+                          int softplus, const float *state_in, float *state_out, void *out, int B,
+                          int D, int N, int G, int dtype, gtr_stream_t stream);
+
+/*
+ * The norms after one block and before the next, fused with the block's gate, its residual
+ * scale and the residual stream.  Per token row (C channels), y the block's output and h the
+ * residual stream:
+ *     p  = y / sqrt(mean_c y^2 + eps) * post_w        (post_w NULL: p = y)
+ *     h' = h + scale * act(gate) * p                  (scale NULL, gate NULL: factor 1)
+ *     n  = h' / sqrt(mean_c h'^2 + eps) * pre_w       (from h' before it is rounded)
+ *   y, n_out [B, L, C] in `dtype`;  h, h_out [B, L, C] in `residual_dtype`, which is `dtype`
+ *     or GTR_F32 (otherwise GTR_ERR_UNSUPPORTED);  h_out may be h, n_out may be y
+ *   gate in `dtype`: [B, C] (one row per sequence) or, with gate_per_token, [B, L, C]; act =
+ *     SiLU where gate_silu is not 0, else the identity
+ *   post_w, pre_w, scale [C] fp32;  pre_w and n_out are both given or both NULL
+ *   eps >= 0 (finite);  C a multiple of 8 up to 16384 (16-bit data) or of 4 up to 8192 (fp32),
+ *     otherwise GTR_ERR_UNSUPPORTED.
+ */
+gtr_status_t gtr_block_norm(const void *y, const void *h, const float *post_w, const float *pre_w,
+                            const void *gate, int gate_per_token, int gate_silu, const float *scale,
+                            float eps, void *h_out, void *n_out, int B, int64_t L, int C, int dtype,
+                            int residual_dtype, gtr_stream_t stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device error word of
  * `workspace` (NULL = the library's cached workspace of the current device).
  * GTR_OK when no device-side failure was recorded.

@@ -266,3 +266,116 @@ def sswiglu_dwconv(xg, xv, conv_w, conv_b, H: int, W: int) -> np.ndarray:
         conv += _f64(conv_b)
     silu = xg / (1.0 + np.exp(-xg))
     return silu * conv.reshape(B, L, C)
+
+
+# ----------------------------------------------------------------------------- selective SSM block
+def _silu(x):
+    return x * np.exp(_log_sigmoid(x))
+
+
+def _full_lengths(lengths, B: int, L: int):
+    return np.full(B, L) if lengths is None else np.clip(np.asarray(lengths, dtype=np.int64), 0, L)
+
+
+def ssm_conv(x, w, bias, H: int, W: int, direction: int = 0, silu: bool = True, state=None, lengths=None):
+    """Short causal depthwise convolution along the scan.
+
+    x [B, L, C], w [C, K], bias [C] or None, state [B, K-1, C] (the inputs before the first
+    position, oldest first) or None.  Returns (out [B, L, C], NaN at positions behind a
+    sequence's length; the last K-1 inputs [B, K-1, C]; the sum of the magnitudes that enter
+    each output's sum [B, L, C]).
+    """
+    x, w = _f64(x), _f64(w)
+    B, L, C = x.shape
+    K = w.shape[1]
+    b = np.zeros(C) if bias is None else _f64(bias)
+    before = np.zeros((B, K - 1, C)) if state is None else _f64(state)
+    order = scan_order(direction, H, W)
+    out, mag = np.full((B, L, C), np.nan), np.full((B, L, C), np.nan)
+    last = np.empty((B, K - 1, C))
+    for i, n in enumerate(_full_lengths(lengths, B, L)):
+        line = np.concatenate([before[i], x[i, order[:n]]])
+        last[i] = line[n:]
+        if n == 0:
+            continue
+        terms = np.stack([line[k:k + n] * w[:, k] for k in range(K)])
+        v = b + terms.sum(0)
+        out[i, order[:n]] = _silu(v) if silu else v
+        mag[i, order[:n]] = np.abs(b) + np.abs(terms).sum(0)
+    return out, last, mag
+
+
+def ssm_scan(u, dt, A, Bm, Cm, H: int, W: int, direction: int = 0, skip=None, z=None, dt_bias=None,
+             softplus: bool = True, state=None, lengths=None, rounding=None):
+    """The selective state space scan, token by token in float64.
+
+        delta_s = softplus(dt_s + dt_bias),  h_s = exp(delta_s A) h_{s-1} + delta_s u_s B_s
+        out_s = (sum_n C_s[n] h_s[n] + skip u_s) SiLU(z_s)
+
+    u, dt, z [B, L, D]; A [D, N]; Bm, Cm [B, L, G, N]; skip, dt_bias [D]; state [B, D, N].
+    Returns (out [B, L, D], NaN behind a sequence's length; state [B, D, N]).
+
+    With ``rounding`` = (per_exp, per_arg, per_input, per_op) also returns bounds on the error of
+    an evaluation in rounded arithmetic (out_err, state_err): an exponential is off by per_exp
+    plus per_arg times the size of its argument, the input delta u B by per_input, each addition
+    to the state and each of the N + 1 terms of the output sum by per_op, all relative to
+    magnitudes that add without cancelling.
+    """
+    u, dt, A, Bm, Cm = _f64(u), _f64(dt), _f64(A), _f64(Bm), _f64(Cm)
+    B, L, D = u.shape
+    N, G = A.shape[1], Bm.shape[2]
+    order = scan_order(direction, H, W)
+    sk = np.zeros(D) if skip is None else _f64(skip)
+    bias = np.zeros(D) if dt_bias is None else _f64(dt_bias)
+    zz = None if z is None else _f64(z)
+    h = np.zeros((B, D, N)) if state is None else _f64(state).copy()
+    n_of = _full_lengths(lengths, B, L)
+    out, oerr = np.full((B, L, D), np.nan), np.full((B, L, D), np.nan)
+    mag, err = np.abs(h), np.zeros_like(h)
+    pe, pa, pi, po = rounding if rounding is not None else (0.0, 0.0, 0.0, 0.0)
+    for s, m in enumerate(order):
+        live = n_of > s
+        if not live.any():
+            break
+        delta = dt[:, m] + bias
+        if softplus:
+            delta = -_log_sigmoid(-delta)
+        arg = delta[..., None] * A
+        a = np.exp(arg)
+        bm = np.repeat(Bm[:, m], D // G, axis=1)
+        cm = np.repeat(Cm[:, m], D // G, axis=1)
+        add = (delta * u[:, m])[..., None] * bm
+        hn = a * h + add
+        y = (hn * cm).sum(-1) + sk * u[:, m]
+        gate = 1.0 if zz is None else _silu(zz[:, m])
+        keep = live[:, None, None]
+        if rounding is not None:
+            m_new = a * mag + np.abs(add)
+            e_new = a * err + a * mag * (pe + pa * np.abs(arg)) + pi * np.abs(add) + po * m_new
+            ey = (np.abs(cm) * (e_new + (N + 1) * po * m_new)).sum(-1) + (N + 1) * po * np.abs(sk * u[:, m])
+            oerr[live, m] = (ey * np.abs(gate) + np.abs(y * gate) * (0.0 if zz is None else pe + pa * np.abs(zz[:, m])
+                             + 4 * po))[live]
+            mag, err = np.where(keep, m_new, mag), np.where(keep, e_new, err)
+        out[live, m] = (y * gate)[live]
+        h = np.where(keep, hn, h)
+    return (out, h) if rounding is None else (out, h, oerr, err)
+
+
+def block_norm(y, h, post_w=None, pre_w=None, gate=None, gate_silu: bool = False, scale=None, eps: float = 1e-6):
+    """h' = h + scale act(gate) RMSNorm(y) post_w and n = RMSNorm(h') pre_w in float64.
+
+    y, h [B, L, C]; gate [B, C] or [B, L, C]; post_w, pre_w, scale [C].  post_w None: no norm of
+    y; pre_w None: n is None.  Returns (h', n, the magnitude |h| + |the block's part| of h').
+    """
+    p, h = _f64(y), _f64(h)
+    if post_w is not None:
+        p = p / np.sqrt((p * p).mean(-1, keepdims=True) + eps) * _f64(post_w)
+    if gate is not None:
+        g = _f64(gate)
+        g = g[:, None, :] if g.ndim == 2 else g
+        p = p * (_silu(g) if gate_silu else g)
+    if scale is not None:
+        p = p * _f64(scale)
+    r = h + p
+    n = None if pre_w is None else r / np.sqrt((r * r).mean(-1, keepdims=True) + eps) * _f64(pre_w)
+    return r, n, np.abs(h) + np.abs(p)
