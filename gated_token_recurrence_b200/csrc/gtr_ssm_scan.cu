@@ -1,11 +1,11 @@
 // Selective state space scan over a prompt, along one of the four scan directions.
 //
 // The recurrence of gtr_ssm.cuh is a chain over time for every (sequence, channel, state).
-// Here a warp takes CW = 32 / TL channels and TL x TS consecutive positions at once: each lane
-// has TS consecutive positions of one channel in registers, and for one state n after the
-// other
-//   1. computes its TS decays a_i = exp(delta_i A) and inputs b_i, and the state h that they
-//      give from zero, with the product of the decays, P = exp(A sum delta_i);
+// Here a warp takes 64 / TL channels and TL x TS consecutive positions at once: each lane has TS
+// consecutive positions of two neighbouring channels in registers, and for one state n after
+// the other
+//   1. computes its decays a_i = exp(delta_i A) and inputs b_i, and the state h that they give
+//      from zero, with the product of the decays, P = exp(A sum delta_i);
 //   2. joins (P, h) with the lanes before it by a shuffle scan over the TL lanes, the state
 //      carried from the previous tile entering at the first lane;
 //   3. runs its TS positions again from the state it now knows, with the same decays, and
@@ -15,17 +15,6 @@
 // another one.  The decays inside a lane enter products of at most TS factors; across lanes
 // and tiles one P stands for TS of them, so the approximate exponential's bias (2e-8) does
 // not build up over a long memory.
-//
-// A CTA of four warps covers 4 CW channels of one sequence and walks along it in tiles of
-// TL x TS positions: rows come in by cp.async (the direction only changes which row comes
-// next; rows behind the sequence's end arrive as zeros), B and C are spread once per tile as
-// fp32 in the order in which the lanes read them, outputs return through the place of u.
-//
-// Bound: the exponential unit.  N exponentials per token and channel at 16 a clock and SM are
-// N / 16 clocks, against 0.35 clocks for the 8 bytes of u, dt, z and out (16-bit data) at the
-// measured HBM bandwidth.
-#include <mutex>
-
 #include "gtr_launch.cuh"
 #include "gtr_ssm.cuh"
 #include "gtr_ssm_host.h"
@@ -35,34 +24,9 @@
 namespace gtr {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxSmem = 227 * 1024;
 
-// Shared memory of one CTA.  Rows of a tile are kept in TL blocks of TS rows with 16 bytes
-// between blocks: the lanes of a warp read the same row of every block at once, and the shift
-// puts them on different banks.
-template <int ES, int TL, int TS>
-struct Layout {
-  int ch_block, n_block;      // bytes from one block of rows to the next: u, dt, z; B, C
-  int ch_tile, n_tile;        // bytes of one tensor's tile
-  int stage;                  // bytes of one stage: u, dt, z, B, C
-  int spread, tokens, table;  // offsets of the fp32 B and C, the token indices, A and carry
-  int total;
-  __host__ __device__ Layout(int N, int stages) {
-    constexpr int kCh = kWarps * 32 / TL;
-    ch_block = TS * kCh * ES + 16;
-    n_block = TS * N * ES + 16;
-    ch_tile = TL * ch_block;
-    n_tile = TL * n_block;
-    stage = 3 * ch_tile + 2 * n_tile;
-    spread = stages * stage;
-    tokens = spread + 2 * N * (TL * TS + 4) * 4;
-    table = tokens + 3 * TL * TS * 4;
-    total = table + 2 * N * kCh * 4;
-  }
-};
-
-// Copy `bytes` (8 or 16) to shared memory asynchronously, or fill with zeros.
+// Copy `BYTES` (8 or 16) to shared memory asynchronously, or fill with zeros.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, bool valid) {
   const uint32_t d = sm100::smem_u32(dst);
@@ -73,238 +37,584 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, bool vali
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
 }
 
-template <typename T, int TL, int TS, int NU>
-__global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const SsmParams p, const int stages) {
-  constexpr int kES = (int)sizeof(T);
-  constexpr int kCW = 32 / TL, kCh = kWarps * kCW, kTT = TL * TS;
-  constexpr int kChBytes = kCh * kES;                      // of one row of u, dt, z
-  constexpr int kPiece = kChBytes < 16 ? kChBytes : 16;    // 8 bytes where a row has no more
-  constexpr int kPieces = kChBytes / kPiece;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const Layout<kES, TL, TS> lay(p.N, stages);
-  float* spread_b = reinterpret_cast<float*>(smem + lay.spread);  // [N][kTT + 4]
-  float* spread_c = spread_b + p.N * (kTT + 4);
-  int* tokens = reinterpret_cast<int*>(smem + lay.tokens);        // [3][kTT]: next, this, last tile
-  float* a_table = reinterpret_cast<float*>(smem + lay.table);    // [N][kCh]: A log2(e)
-  float* carry = a_table + p.N * kCh;                             // [N][kCh]: h so far
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 r, a, b;\n\t"
+      "mov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tl = lane % TL, cw = lane / TL;
-  const int c = warp * kCW + cw;  // channel within the CTA
-  const int d0 = blockIdx.x * kCh, b = blockIdx.y;
-  const int g = d0 / (p.D / p.G);
-
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  const int len = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.L) : p.L;
-  const int tiles = (len + kTT - 1) / kTT;
-  for (int i = tid; i < p.N * kCh; i += kThreads) {
-    const int ch = i / p.N, n = i - ch * p.N;
-    a_table[n * kCh + ch] = __ldg(p.A + (long long)(d0 + ch) * p.N + n) * kLog2e;
-    carry[n * kCh + ch] = p.state_in ? p.state_in[((long long)b * p.D + d0 + ch) * p.N + n] : 0.f;
+// Two neighbouring channels of a row.
+template <typename T> struct Pair;
+template <> struct Pair<__half> {
+  static __device__ __forceinline__ float2 load(const void* p) { return __half22float2(*static_cast<const __half2*>(p)); }
+  static __device__ __forceinline__ void store(void* p, float2 f) { *static_cast<__half2*>(p) = __floats2half2_rn(f.x, f.y); }
+  using Raw = uint32_t;
+};
+template <> struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 load(const void* p) {
+    const uint32_t w = *static_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  const float skip = p.skip ? __ldg(p.skip + d0 + c) : 0.f;
-  const float bias = p.dt_bias ? __ldg(p.dt_bias + d0 + c) : 0.f;
+  static __device__ __forceinline__ void store(void* p, float2 f) {
+    *static_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(f.x, f.y);
+  }
+  using Raw = uint32_t;
+};
+template <> struct Pair<float> {
+  static __device__ __forceinline__ float2 load(const void* p) { return *static_cast<const float2*>(p); }
+  static __device__ __forceinline__ void store(void* p, float2 f) { *static_cast<float2*>(p) = f; }
+  using Raw = uint2;
+};
 
-  const auto set_tokens = [&](int tile) {
-    for (int r = tid; r < kTT; r += kThreads) {
+// The tile of TL x TS positions of CH channels in shared memory.  Raw rows are kept in TL
+// blocks of TS rows with a gap between blocks: the lanes of a warp read the same row of every
+// block at once, and the shift puts them on different banks.  Position t = l TS + 4 q + r of
+// a table over positions is at place (q TL + l) 4 + r, the order of the lanes' 16-byte reads.
+template <typename T, int TL, int TS, int CH>
+struct Tile {
+  static constexpr int kES = (int)sizeof(T);
+  static constexpr int kTT = TL * TS;
+  static constexpr int kRow = CH * kES;                            // bytes of a row of u, dt, z
+  static constexpr int kBlock = TS * kRow + (kRow < 16 ? 8 : 16);  // one block of rows
+  static constexpr int kRaw = (TL * kBlock + 15) / 16 * 16;        // u, dt or z
+  static constexpr int kPiece = kRow < 16 ? kRow : 16;             // 8 bytes where a row has no more
+  static constexpr int kPieces = kRow / kPiece;
+  static constexpr int kN = 16 / kES;
+  static constexpr int kPlaces = kTT + 4;  // of one state in a table
+
+  static __host__ __device__ int n_block(int N) { return TS * N * kES + 16; }
+  static __host__ __device__ int raw_n(int N) { return TL * n_block(N); }                 // B or C
+  static __host__ __device__ int stage(int N) { return 3 * kRaw + 2 * raw_n(N); }
+  static __host__ __device__ int spread(int N) { return 2 * N * kPlaces * 4; }            // B and C as fp32
+  static __device__ __forceinline__ int position(int place) {
+    return ((place / 4) % TL) * TS + (place / (4 * TL)) * 4 + place % 4;
+  }
+  static __device__ __forceinline__ int raw_at(int t) { return (t / TS) * kBlock + (t % TS) * kRow; }
+
+  static __device__ __forceinline__ void set_tokens(const SsmParams& p, int* tok, int tile, int len, int tid, int threads) {
+    for (int r = tid; r < kTT; r += threads) {
       const int s = tile * kTT + r;
-      tokens[(tile % 3) * kTT + r] = s < len ? p.map.token((unsigned)s) : -1;
+      tok[r] = s < len ? p.map.token((unsigned)s) : -1;
     }
-  };
-  const long long row0 = (long long)b * p.L;
-  const auto load_tile = [&](int tile) {
-    uint8_t* st = smem + (stages == 2 ? (tile & 1) * lay.stage : 0);
-    const int* tok = tokens + (tile % 3) * kTT;
-    for (int i = tid; i < kTT * kPieces; i += kThreads) {
+  }
+  // Request a tile's rows; rows behind the sequence's end arrive as zeros.
+  static __device__ __forceinline__ void load(const SsmParams& p, uint8_t* st, const int* tok, long long row0, int d0,
+                                              int g, int tid, int threads) {
+    for (int i = tid; i < kTT * kPieces; i += threads) {
       const int r = i / kPieces, q = i - r * kPieces;
       const int m = tok[r];
       const long long row = row0 + max(m, 0);
-      const int off = (r / TS) * lay.ch_block + (r % TS) * kChBytes + q * kPiece;
+      uint8_t* dst = st + raw_at(r) + q * kPiece;
       const int e = d0 + q * (kPiece / kES);
-      copy_async<kPiece>(st + off, static_cast<const T*>(p.u) + row * p.u_ld + e, m >= 0);
-      copy_async<kPiece>(st + lay.ch_tile + off, static_cast<const T*>(p.dt) + row * p.dt_ld + e, m >= 0);
-      if (p.z) copy_async<kPiece>(st + 2 * lay.ch_tile + off, static_cast<const T*>(p.z) + row * p.z_ld + e, m >= 0);
+      copy_async<kPiece>(dst, static_cast<const T*>(p.u) + row * p.u_ld + e, m >= 0);
+      copy_async<kPiece>(dst + kRaw, static_cast<const T*>(p.dt) + row * p.dt_ld + e, m >= 0);
+      if (p.z) copy_async<kPiece>(dst + 2 * kRaw, static_cast<const T*>(p.z) + row * p.z_ld + e, m >= 0);
     }
-    const int np = p.N * kES / 16;
-    for (int i = tid; i < kTT * np; i += kThreads) {
-      const int r = i / np, q = i - r * np;
+    const int np = p.N / kN, rn = raw_n(p.N);
+    for (int r = tid; r < kTT; r += threads) {
       const int m = tok[r];
       const long long row = row0 + max(m, 0);
-      const int off = 3 * lay.ch_tile + (r / TS) * lay.n_block + (r % TS) * p.N * kES + q * 16;
-      const int e = g * p.N + q * (16 / kES);
-      copy_async<16>(st + off, static_cast<const T*>(p.Bm) + row * p.bm_ld + e, m >= 0);
-      copy_async<16>(st + lay.n_tile + off, static_cast<const T*>(p.Cm) + row * p.cm_ld + e, m >= 0);
+      uint8_t* dst = st + 3 * kRaw + (r / TS) * n_block(p.N) + (r % TS) * p.N * kES;
+      const T* bm = static_cast<const T*>(p.Bm) + row * p.bm_ld + g * p.N;
+      const T* cm = static_cast<const T*>(p.Cm) + row * p.cm_ld + g * p.N;
+      for (int q = 0; q < np; ++q) {
+        copy_async<16>(dst + 16 * q, bm + q * kN, m >= 0);
+        copy_async<16>(dst + rn + 16 * q, cm + q * kN, m >= 0);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-
-  if (tiles > 0) {
-    set_tokens(0);
-    __syncthreads();
-    load_tile(0);
   }
+  // B and C as fp32, state by state.
+  static __device__ __forceinline__ void spread_bc(int N, const uint8_t* st, float* table, int tid, int threads) {
+    const int np = N / kN, rn = raw_n(N), nb = n_block(N);
+    for (int i = tid; i < kTT * np; i += threads) {
+      const int piece = i / kTT, k = i - piece * kTT;
+      const int r = position(k);
+      const uint8_t* src = st + 3 * kRaw + (r / TS) * nb + (r % TS) * N * kES + piece * 16;
+      float f[kN], h[kN];
+      Vec8<T>::load(*reinterpret_cast<const uint4*>(src), f);
+      Vec8<T>::load(*reinterpret_cast<const uint4*>(src + rn), h);
+      float* dst = table + piece * kN * kPlaces + k;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        dst[e * kPlaces] = f[e];
+        dst[(N + e) * kPlaces] = h[e];
+      }
+    }
+  }
+};
+
+// What a lane has of a tile: TS positions of two channels.
+template <int TL, int TS>
+struct Chains {
+  float dl[2][TS], du[2][TS], y[2][TS], sum[2];
+
+  // The decays of one state, and P.
+  __device__ __forceinline__ void decays(const float* a_row, float2 (&a)[2][TS / 2], float (&P)[2]) const {
+    const float2 A = *reinterpret_cast<const float2*>(a_row);
+    P[0] = exp2_approx(sum[0] * A.x);
+    P[1] = exp2_approx(sum[1] * A.y);
+#pragma unroll
+    for (int i = 0; i < TS / 2; ++i)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const float2 e = mul2(make_float2(dl[v][2 * i], dl[v][2 * i + 1]), v ? make_float2(A.y, A.y) : make_float2(A.x, A.x));
+        a[v][i] = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+      }
+  }
+
+  // One state: b_row, c_row this lane's B and C, h_row the carried state of its two channels,
+  // next_row the following state's decay rates (NEXT): its exponentials are computed while
+  // this state's shuffles and chains wait for one another.
+  template <bool NEXT>
+  __device__ __forceinline__ void state(int tl, const float4* b_row, const float4* c_row, float* h_row, const float* next_row,
+                                        const float2 (&a)[2][TS / 2], float (&P)[2], float2 (&a_next)[2][TS / 2],
+                                        float (&P_next)[2]) {
+    float2 bb[2][TS / 2];
+    const float2 old = *reinterpret_cast<const float2*>(h_row);
+    const float in[2] = {old.x, old.y};
+#pragma unroll
+    for (int q = 0; q < TS / 4; ++q) {
+      const float4 f = b_row[q * TL];
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        bb[v][2 * q] = mul2(make_float2(du[v][4 * q], du[v][4 * q + 1]), make_float2(f.x, f.y));
+        bb[v][2 * q + 1] = mul2(make_float2(du[v][4 * q + 2], du[v][4 * q + 3]), make_float2(f.z, f.w));
+      }
+    }
+    float h[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < TS / 2; ++i) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) h[v] = fmaf(a[v][i].x, h[v], bb[v][i].x);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) h[v] = fmaf(a[v][i].y, h[v], bb[v][i].y);
+    }
+    if (tl == 0) {
+      h[0] = fmaf(P[0], in[0], h[0]);
+      h[1] = fmaf(P[1], in[1], h[1]);
+    }
+    __syncwarp();  // every lane has the old carry
+    if constexpr (NEXT) decays(next_row, a_next, P_next);
+#pragma unroll
+    for (int s = 1; s < TL; s *= 2) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const float hp = __shfl_up_sync(0xffffffffu, h[v], s, TL);
+        if (tl >= s) h[v] = fmaf(P[v], hp, h[v]);
+        if (2 * s < TL) {
+          const float Pp = __shfl_up_sync(0xffffffffu, P[v], s, TL);
+          if (tl >= s) P[v] *= Pp;
+        }
+      }
+    }
+    float x[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const float hp = __shfl_up_sync(0xffffffffu, h[v], 1, TL);
+      x[v] = tl > 0 ? hp : in[v];
+    }
+#pragma unroll
+    for (int q = 0; q < TS / 4; ++q) {
+      const float4 f = c_row[q * TL];
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        float2 h0, h1;
+        h0.x = fmaf(a[v][2 * q].x, x[v], bb[v][2 * q].x);
+        h0.y = fmaf(a[v][2 * q].y, h0.x, bb[v][2 * q].y);
+        h1.x = fmaf(a[v][2 * q + 1].x, h0.y, bb[v][2 * q + 1].x);
+        h1.y = x[v] = fmaf(a[v][2 * q + 1].y, h1.x, bb[v][2 * q + 1].y);
+        const float2 y0 = fma2(h0, make_float2(f.x, f.y), make_float2(y[v][4 * q], y[v][4 * q + 1]));
+        const float2 y1 = fma2(h1, make_float2(f.z, f.w), make_float2(y[v][4 * q + 2], y[v][4 * q + 3]));
+        y[v][4 * q] = y0.x, y[v][4 * q + 1] = y0.y, y[v][4 * q + 2] = y1.x, y[v][4 * q + 3] = y1.y;
+      }
+    }
+    if (tl == TL - 1) *reinterpret_cast<float2*>(h_row) = make_float2(x[0], x[1]);
+  }
+
+  // The states n0, n0 + step, ... of N: tables of the tile, rows of CH channels, this lane's
+  // first channel c.
+  template <int CH>
+  __device__ __forceinline__ void states(int N, int n0, int step, int tl, int c, const float* table, const float* a_table,
+                                         float* carry) {
+    constexpr int kPlaces = TL * TS + 4;
+    float2 a0[2][TS / 2], a1[2][TS / 2];
+    float P0[2], P1[2];
+    const auto b_row = [&](int n) { return reinterpret_cast<const float4*>(table + n * kPlaces) + tl; };
+    const auto c_row = [&](int n) { return reinterpret_cast<const float4*>(table + (N + n) * kPlaces) + tl; };
+    decays(a_table + n0 * CH + c, a0, P0);
+    for (int n = n0;; n += 2 * step) {
+      const int m = n + step;
+      if (m >= N) {
+        state<false>(tl, b_row(n), c_row(n), carry + n * CH + c, nullptr, a0, P0, a1, P1);
+        break;
+      }
+      state<true>(tl, b_row(n), c_row(n), carry + n * CH + c, a_table + m * CH + c, a0, P0, a1, P1);
+      if (m + step >= N) {
+        state<false>(tl, b_row(m), c_row(m), carry + m * CH + c, nullptr, a1, P1, a0, P0);
+        break;
+      }
+      state<true>(tl, b_row(m), c_row(m), carry + m * CH + c, a_table + (m + step) * CH + c, a1, P1, a0, P0);
+    }
+  }
+};
+
+// The tables that live as long as the block, [N][CH]: A log2(e) and the carried states.
+template <int CH>
+__device__ __forceinline__ void load_tables(const SsmParams& p, float* a_table, float* carry, int d0, int b, int tid,
+                                            int threads) {
+  for (int i = tid; i < p.N * CH; i += threads) {
+    const int ch = i / p.N, n = i - ch * p.N;
+    a_table[n * CH + ch] = __ldg(p.A + (long long)(d0 + ch) * p.N + n) * kLog2e;
+    carry[n * CH + ch] = p.state_in ? p.state_in[((long long)b * p.D + d0 + ch) * p.N + n] : 0.f;
+  }
+}
+template <int CH>
+__device__ __forceinline__ void store_states(const SsmParams& p, const float* carry, int d0, int b, int tid, int threads) {
+  for (int i = tid; i < p.N * CH; i += threads) {
+    const int ch = i / p.N, n = i - ch * p.N;
+    p.state_out[((long long)b * p.D + d0 + ch) * p.N + n] = carry[n * CH + ch];
+  }
+}
+__device__ __forceinline__ float2 channel_pair(const float* v, int ch) {
+  return v ? make_float2(__ldg(v + ch), __ldg(v + ch + 1)) : make_float2(0.f, 0.f);
+}
+__device__ __forceinline__ int sequence_length(const SsmParams& p, int b) {
+  return p.lengths ? min(max(__ldg(p.lengths + b), 0), p.L) : p.L;
+}
+
+// ------------------------------------------------------------------------------- many channels
+// WC warps of 64 / TL channels each: every warp does all states of its channels, and the phases
+// of one block (copies, tables, states, outputs) overlap with those of the other blocks on
+// the SM.
+template <typename T, int TL, int TS, int WC>
+struct WideLayout {
+  using Tl = Tile<T, TL, TS, WC * 64 / TL>;
+  int spread, hold, tokens, table, total;  // the raw tile is at 0
+  __host__ __device__ explicit WideLayout(int N) {
+    spread = Tl::stage(N);
+    hold = spread + Tl::spread(N);  // z, then the outputs
+    tokens = hold + Tl::kRaw;       // [3][kTT]: next, this, last tile
+    table = tokens + 3 * Tl::kTT * 4;
+    total = table + 2 * N * (WC * 64 / TL) * 4;
+  }
+};
+
+template <typename T, int TL, int TS, int WC, int MB>
+__global__ void __launch_bounds__(32 * WC, MB) ssm_scan_wide_kernel(const SsmParams p) {
+  constexpr int kThreads = 32 * WC, kCh = WC * 64 / TL;
+  using Tl = Tile<T, TL, TS, kCh>;
+  constexpr int kTT = Tl::kTT, kES = Tl::kES, kPiece = Tl::kPiece, kPieces = Tl::kPieces;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const WideLayout<T, TL, TS, WC> lay(p.N);
+  float* table = reinterpret_cast<float*>(smem + lay.spread);
+  int* tokens = reinterpret_cast<int*>(smem + lay.tokens);
+  float* a_table = reinterpret_cast<float*>(smem + lay.table);
+  float* carry = a_table + p.N * kCh;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int tl = lane % TL;
+  const int c = ((tid >> 5) * (32 / TL) + lane / TL) * 2;  // the first of this lane's channels
+  const int d0 = blockIdx.x * kCh, b = blockIdx.y;
+  const int g = d0 / (p.D / p.G);
+  const long long row0 = (long long)b * p.L;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int len = sequence_length(p, b), tiles = (len + kTT - 1) / kTT;
+  load_tables<kCh>(p, a_table, carry, d0, b, tid, kThreads);
+  if (tiles > 0) {
+    Tl::set_tokens(p, tokens, 0, len, tid, kThreads);
+    __syncthreads();
+    Tl::load(p, smem, tokens, row0, d0, g, tid, kThreads);
+  }
+  const float2 skip = channel_pair(p.skip, d0 + c), bias = channel_pair(p.dt_bias, d0 + c);
+  const uint8_t* raw = smem + tl * Tl::kBlock + c * kES;
+  uint8_t* hold = smem + lay.hold + tl * Tl::kBlock + c * kES;
   for (int tile = 0; tile < tiles; ++tile) {
     const bool more = tile + 1 < tiles;
-    uint8_t* st = smem + (stages == 2 ? (tile & 1) * lay.stage : 0);
-    if (more) set_tokens(tile + 1);
+    const int* tok = tokens + (tile % 3) * kTT;
+    int* tok_next = tokens + ((tile + 1) % 3) * kTT;
+    if (more) Tl::set_tokens(p, tok_next, tile + 1, len, tid, kThreads);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();  // this tile is here; the other stage's outputs have left; tokens are set
-    if (stages == 2 && more) load_tile(tile + 1);
-
-    // B and C as fp32, state by state in the order of the lanes' 16-byte reads: position
-    // t = l TS + 4 q + r of the tile at (q TL + l) 4 + r
-    {
-      const int np = p.N * kES / 16;
-      for (int i = tid; i < kTT * np; i += kThreads) {
-        const int piece = i / kTT, k = i - piece * kTT;  // k: place in that order
-        const int r = ((k / 4) % TL) * TS + (k / (4 * TL)) * 4 + k % 4;
-        const uint8_t* src = st + 3 * lay.ch_tile + (r / TS) * lay.n_block + (r % TS) * p.N * kES + piece * 16;
-        float f[16 / kES], h[16 / kES];
-        Vec8<T>::load(*reinterpret_cast<const uint4*>(src), f);
-        Vec8<T>::load(*reinterpret_cast<const uint4*>(src + lay.n_tile), h);
+    __syncthreads();  // the tile is here, its predecessor's outputs have left, tokens are set
+    Tl::spread_bc(p.N, smem, table, tid, kThreads);
+    Chains<TL, TS> ch;
 #pragma unroll
-        for (int e = 0; e < 16 / kES; ++e) {
-          spread_b[(piece * (16 / kES) + e) * (kTT + 4) + k] = f[e];
-          spread_c[(piece * (16 / kES) + e) * (kTT + 4) + k] = h[e];
-        }
+    for (int i = 0; i < TS; ++i) {
+      const float2 x = Pair<T>::load(raw + Tl::kRaw + i * Tl::kRow);
+      ch.dl[0][i] = x.x + bias.x;
+      ch.dl[1][i] = x.y + bias.y;
+    }
+    if (p.softplus) {  // one branch around them all, so that they overlap
+#pragma unroll
+      for (int i = 0; i < TS; ++i) {
+        ch.dl[0][i] = softplus_f32(ch.dl[0][i]);
+        ch.dl[1][i] = softplus_f32(ch.dl[1][i]);
       }
     }
-    // this lane's positions
-    float dl[TS], du[TS], y[TS], sum = 0.f;
-    T* up = reinterpret_cast<T*>(st + tl * lay.ch_block) + c;
-    const T* dp = reinterpret_cast<const T*>(st + lay.ch_tile + tl * lay.ch_block) + c;
     const int left = len - tile * kTT - tl * TS;  // positions of the sequence from here on
+    ch.sum[0] = ch.sum[1] = 0.f;
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
-      const float u = Elem<T>::to_f32(up[i * kCh]);
-      float x = Elem<T>::to_f32(dp[i * kCh]) + bias;
-      if (p.softplus) x = softplus_f32(x);
-      dl[i] = i < left ? x : 0.f;
-      du[i] = dl[i] * u;
-      y[i] = skip * u;
-      sum += dl[i];
+      const float2 u = Pair<T>::load(raw + i * Tl::kRow);
+      if (i >= left) ch.dl[0][i] = ch.dl[1][i] = 0.f;
+      ch.du[0][i] = ch.dl[0][i] * u.x;
+      ch.du[1][i] = ch.dl[1][i] * u.y;
+      ch.y[0][i] = skip.x * u.x;
+      ch.y[1][i] = skip.y * u.y;
+      ch.sum[0] += ch.dl[0][i];
+      ch.sum[1] += ch.dl[1][i];
     }
-    __syncthreads();  // B and C are spread
-
-    for (int n0 = 0; n0 < p.N; n0 += NU) {
-      float a[NU][TS], bb[NU][TS], h[NU], P[NU], in[NU];
+    if (p.z) {
+      using Raw = typename Pair<T>::Raw;
 #pragma unroll
-      for (int v = 0; v < NU; ++v) {
-        const float A = a_table[(n0 + v) * kCh + c];
-        in[v] = carry[(n0 + v) * kCh + c];
-        const float4* bp = reinterpret_cast<const float4*>(spread_b + (n0 + v) * (kTT + 4)) + tl;
-        P[v] = exp2_approx(sum * A);
-        h[v] = 0.f;
+      for (int i = 0; i < TS; ++i)
+        *reinterpret_cast<Raw*>(hold + i * Tl::kRow) = *reinterpret_cast<const Raw*>(raw + 2 * Tl::kRaw + i * Tl::kRow);
+    }
+    __syncthreads();  // B and C are spread, the raw tile has been read
+    if (more) Tl::load(p, smem, tok_next, row0, d0, g, tid, kThreads);
+    ch.template states<kCh>(p.N, 0, 1, tl, c, table, a_table, carry);
+    if (p.z) {
 #pragma unroll
-        for (int q = 0; q < TS / 4; ++q) {
-          const float4 f = bp[q * TL];
-          bb[v][4 * q] = du[4 * q] * f.x;
-          bb[v][4 * q + 1] = du[4 * q + 1] * f.y;
-          bb[v][4 * q + 2] = du[4 * q + 2] * f.z;
-          bb[v][4 * q + 3] = du[4 * q + 3] * f.w;
-        }
-#pragma unroll
-        for (int i = 0; i < TS; ++i) a[v][i] = exp2_approx(dl[i] * A);
-#pragma unroll
-        for (int i = 0; i < TS; ++i) h[v] = fmaf(a[v][i], h[v], bb[v][i]);
-        if (tl == 0) h[v] = fmaf(P[v], in[v], h[v]);
-      }
-      __syncwarp();  // every lane has the old carry
-#pragma unroll
-      for (int s = 1; s < TL; s *= 2) {
-#pragma unroll
-        for (int v = 0; v < NU; ++v) {
-          const float hp = __shfl_up_sync(0xffffffffu, h[v], s, TL);
-          if (tl >= s) h[v] = fmaf(P[v], hp, h[v]);
-          if (2 * s < TL) {
-            const float Pp = __shfl_up_sync(0xffffffffu, P[v], s, TL);
-            if (tl >= s) P[v] *= Pp;
-          }
-        }
-      }
-#pragma unroll
-      for (int v = 0; v < NU; ++v) {
-        const float hp = __shfl_up_sync(0xffffffffu, h[v], 1, TL);
-        if (tl > 0) in[v] = hp;
-        const float4* cp = reinterpret_cast<const float4*>(spread_c + (n0 + v) * (kTT + 4)) + tl;
-#pragma unroll
-        for (int q = 0; q < TS / 4; ++q) {
-          const float4 f = cp[q * TL];
-          in[v] = fmaf(a[v][4 * q], in[v], bb[v][4 * q]);
-          y[4 * q] = fmaf(f.x, in[v], y[4 * q]);
-          in[v] = fmaf(a[v][4 * q + 1], in[v], bb[v][4 * q + 1]);
-          y[4 * q + 1] = fmaf(f.y, in[v], y[4 * q + 1]);
-          in[v] = fmaf(a[v][4 * q + 2], in[v], bb[v][4 * q + 2]);
-          y[4 * q + 2] = fmaf(f.z, in[v], y[4 * q + 2]);
-          in[v] = fmaf(a[v][4 * q + 3], in[v], bb[v][4 * q + 3]);
-          y[4 * q + 3] = fmaf(f.w, in[v], y[4 * q + 3]);
-        }
-        if (tl == TL - 1) carry[(n0 + v) * kCh + c] = in[v];
+      for (int i = 0; i < TS; ++i) {
+        const float2 z = Pair<T>::load(hold + i * Tl::kRow);
+        ch.y[0][i] *= ssm_silu(z.x);
+        ch.y[1][i] *= ssm_silu(z.y);
       }
     }
-    const T* zp = reinterpret_cast<const T*>(st + 2 * lay.ch_tile + tl * lay.ch_block) + c;
 #pragma unroll
-    for (int i = 0; i < TS; ++i) {
-      if (p.z) y[i] *= ssm_silu(Elem<T>::to_f32(zp[i * kCh]));
-      up[i * kCh] = Elem<T>::from_f32(y[i]);
-    }
-    __syncthreads();  // outputs are in the place of u; the spread B and C have been read
-    {
-      const int* tok = tokens + (tile % 3) * kTT;
-      for (int i = tid; i < kTT * kPieces; i += kThreads) {
-        const int r = i / kPieces, q = i - r * kPieces;
-        const int m = tok[r];
-        if (m < 0) continue;
-        const uint8_t* src = st + (r / TS) * lay.ch_block + (r % TS) * kChBytes + q * kPiece;
-        T* dst = static_cast<T*>(p.out) + (row0 + m) * p.D + d0 + q * (kPiece / kES);
-        if constexpr (kPiece == 16)
-          *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-        else
-          *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src);
-      }
-    }
-    if (stages == 1 && more) {
-      __syncthreads();  // the stage is free
-      load_tile(tile + 1);
+    for (int i = 0; i < TS; ++i) Pair<T>::store(hold + i * Tl::kRow, make_float2(ch.y[0][i], ch.y[1][i]));
+    __syncthreads();  // the outputs are there; the spread B and C have been read
+    for (int i = tid; i < kTT * kPieces; i += kThreads) {
+      const int r = i / kPieces, q = i - r * kPieces;
+      const int m = tok[r];
+      if (m < 0) continue;
+      const uint8_t* src = smem + lay.hold + Tl::raw_at(r) + q * kPiece;
+      T* dst = static_cast<T*>(p.out) + (row0 + m) * p.D + d0 + q * (kPiece / kES);
+      if constexpr (kPiece == 16)
+        *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+      else
+        *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src);
     }
   }
   if (p.state_out) {
     __syncthreads();
-    for (int i = tid; i < p.N * kCh; i += kThreads) {
-      const int ch = i / p.N, n = i - ch * p.N;
-      p.state_out[((long long)b * p.D + d0 + ch) * p.N + n] = carry[n * kCh + ch];
+    store_states<kCh>(p, carry, d0, b, tid, kThreads);
+  }
+}
+
+// -------------------------------------------------------------------------------- few channels
+// One block on an SM: WC groups of channels times SG groups of states, a warp each, run the
+// states of one tile while WP other warps copy and prepare the next one (B, C, delta and delta
+// u as fp32 tables) and finish the last one (the sum over the state groups, skip, gate).
+// Tables and partial outputs are doubled, raw tiles (u and z are read again at the end) are three; the two sides meet at named barriers: ready[k & 1]
+// (tile k's tables are there; partial outputs k - 2 have been read) and done[k & 1] (partial
+// outputs k are there; tile k's tables have been read).
+template <typename T, int TL, int TS, int WC, int SG>
+struct DeepLayout {
+  static constexpr int kCh = WC * 64 / TL;
+  using Tl = Tile<T, TL, TS, kCh>;
+  static constexpr int kStride = Tl::kTT + 4;  // of one channel: a warp's channels on other banks
+  static constexpr int kDelta = 2 * kCh * kStride * 4;  // delta and delta u
+  static constexpr int kPart = SG * kCh * kStride * 4;
+  int stage, spread, delta, part, tokens, table, total;  // [3] raw stages at 0
+  __host__ __device__ explicit DeepLayout(int N) {
+    stage = Tl::stage(N);
+    spread = 3 * stage;                      // [2]
+    delta = spread + 2 * Tl::spread(N);      // [2]
+    part = delta + 2 * kDelta;               // [2]
+    tokens = part + 2 * kPart;               // [4][kTT]
+    table = tokens + 4 * Tl::kTT * 4;
+    total = table + 2 * N * kCh * 4;
+  }
+};
+
+template <int THREADS>
+__device__ __forceinline__ void bar_sync(int id) {
+  asm volatile("barrier.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
+}
+template <int THREADS>
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("barrier.arrive %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
+}
+
+template <typename T, int TL, int TS, int WC, int SG, int WP>
+__global__ void __launch_bounds__(32 * (WC * SG + WP), 1) ssm_scan_deep_kernel(const SsmParams p) {
+  constexpr int kCh = WC * 64 / TL;
+  constexpr int kPrep = 32 * WP, kAll = 32 * (WC * SG + WP);
+  constexpr int kReady = 1, kDone = 3, kPrepBar = 5;  // barrier numbers; ready and done: + (tile & 1)
+  using Tl = Tile<T, TL, TS, kCh>;
+  using Lay = DeepLayout<T, TL, TS, WC, SG>;
+  constexpr int kTT = Tl::kTT, kES = Tl::kES, kStride = Lay::kStride;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Lay lay(p.N);
+  int* tokens = reinterpret_cast<int*>(smem + lay.tokens);
+  float* a_table = reinterpret_cast<float*>(smem + lay.table);
+  float* carry = a_table + p.N * kCh;
+  const int tid = threadIdx.x;
+  const int d0 = blockIdx.x * kCh, b = blockIdx.y;
+  const int g = d0 / (p.D / p.G);
+  const long long row0 = (long long)b * p.L;
+  const int spread_bytes = Tl::spread(p.N);
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int len = sequence_length(p, b), tiles = (len + kTT - 1) / kTT;
+  load_tables<kCh>(p, a_table, carry, d0, b, tid, kAll);
+  __syncthreads();
+
+  if (tid < kPrep) {
+    const int pc = 2 * (tid % (kCh / 2));  // the channels that this thread prepares and finishes
+    const float2 skip = channel_pair(p.skip, d0 + pc), bias = channel_pair(p.dt_bias, d0 + pc);
+    if (tiles > 0) {
+      Tl::set_tokens(p, tokens, 0, len, tid, kPrep);
+      bar_sync<kPrep>(kPrepBar);
+      Tl::load(p, smem, tokens, row0, d0, g, tid, kPrep);
+    }
+    for (int tile = 0; tile <= tiles; ++tile) {
+      if (tile < tiles) {
+        const uint8_t* st = smem + (tile % 3) * lay.stage;
+        const bool more = tile + 1 < tiles;
+        int* tok_next = tokens + ((tile + 1) & 3) * kTT;
+        if (more) Tl::set_tokens(p, tok_next, tile + 1, len, tid, kPrep);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        bar_sync<kPrep>(kPrepBar);  // the tile is here, tokens are set, tile - 2 is finished
+        if (more) Tl::load(p, smem + ((tile + 1) % 3) * lay.stage, tok_next, row0, d0, g, tid, kPrep);
+        Tl::spread_bc(p.N, st, reinterpret_cast<float*>(smem + lay.spread + (tile & 1) * spread_bytes), tid, kPrep);
+        float* delta = reinterpret_cast<float*>(smem + lay.delta + (tile & 1) * Lay::kDelta);
+#pragma unroll 2
+        for (int k = tid / (kCh / 2); k < kTT; k += kPrep / (kCh / 2)) {
+          const int r = Tl::position(k);
+          const uint8_t* at = st + Tl::raw_at(r) + pc * kES;
+          const float2 u = Pair<T>::load(at), x = Pair<T>::load(at + Tl::kRaw);
+          float e = x.x + bias.x, f = x.y + bias.y;
+          if (p.softplus) e = softplus_f32(e), f = softplus_f32(f);
+          if (tile * kTT + r >= len) e = f = 0.f;
+          delta[pc * kStride + k] = e;
+          delta[(pc + 1) * kStride + k] = f;
+          delta[(kCh + pc) * kStride + k] = e * u.x;
+          delta[(kCh + pc + 1) * kStride + k] = f * u.y;
+        }
+        bar_arrive<kAll>(kReady + (tile & 1));
+      }
+      if (tile > 0) {  // finish the last tile
+        const int last = tile - 1;
+        const uint8_t* st = smem + (last % 3) * lay.stage;
+        const int* tok = tokens + (last & 3) * kTT;
+        const float* part = reinterpret_cast<const float*>(smem + lay.part + (last & 1) * Lay::kPart);
+        bar_sync<kAll>(kDone + (last & 1));
+#pragma unroll 2
+        for (int k = tid / (kCh / 2); k < kTT; k += kPrep / (kCh / 2)) {
+          const int r = Tl::position(k);
+          const int m = tok[r];
+          const uint8_t* at = st + Tl::raw_at(r) + pc * kES;
+          const float2 u = Pair<T>::load(at);
+          float2 v = make_float2(skip.x * u.x, skip.y * u.y);
+#pragma unroll
+          for (int s = 0; s < SG; ++s) {
+            v.x += part[(s * kCh + pc) * kStride + k];
+            v.y += part[(s * kCh + pc + 1) * kStride + k];
+          }
+          if (p.z) {
+            const float2 z = Pair<T>::load(at + 2 * Tl::kRaw);
+            v.x *= ssm_silu(z.x);
+            v.y *= ssm_silu(z.y);
+          }
+          if (m >= 0) Pair<T>::store(static_cast<T*>(p.out) + (row0 + m) * p.D + d0 + pc, v);
+        }
+      }
+    }
+  } else {
+    const int lane = tid & 31, warp = (tid - kPrep) >> 5;
+    const int tl = lane % TL;
+    const int c = ((warp % WC) * (32 / TL) + lane / TL) * 2;
+    const int sg = warp / WC;
+    for (int tile = 0; tile < tiles; ++tile) {
+      bar_sync<kAll>(kReady + (tile & 1));
+      const float* delta = reinterpret_cast<const float*>(smem + lay.delta + (tile & 1) * Lay::kDelta);
+      Chains<TL, TS> ch;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        ch.sum[v] = 0.f;
+#pragma unroll
+        for (int q = 0; q < TS / 4; ++q) {
+          const float4 f = *reinterpret_cast<const float4*>(delta + (c + v) * kStride + (q * TL + tl) * 4);
+          const float4 h = *reinterpret_cast<const float4*>(delta + (kCh + c + v) * kStride + (q * TL + tl) * 4);
+          ch.dl[v][4 * q] = f.x, ch.dl[v][4 * q + 1] = f.y, ch.dl[v][4 * q + 2] = f.z, ch.dl[v][4 * q + 3] = f.w;
+          ch.du[v][4 * q] = h.x, ch.du[v][4 * q + 1] = h.y, ch.du[v][4 * q + 2] = h.z, ch.du[v][4 * q + 3] = h.w;
+          ch.sum[v] += (f.x + f.y) + (f.z + f.w);
+          ch.y[v][4 * q] = ch.y[v][4 * q + 1] = ch.y[v][4 * q + 2] = ch.y[v][4 * q + 3] = 0.f;
+        }
+      }
+      ch.template states<kCh>(p.N, sg, SG, tl, c, reinterpret_cast<const float*>(smem + lay.spread + (tile & 1) * spread_bytes),
+                              a_table, carry);
+      float* part = reinterpret_cast<float*>(smem + lay.part + (tile & 1) * Lay::kPart) + sg * kCh * kStride;
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int q = 0; q < TS / 4; ++q)
+          *reinterpret_cast<float4*>(part + (c + v) * kStride + (q * TL + tl) * 4) =
+              make_float4(ch.y[v][4 * q], ch.y[v][4 * q + 1], ch.y[v][4 * q + 2], ch.y[v][4 * q + 3]);
+      bar_arrive<kAll>(kDone + (tile & 1));
     }
   }
+  if (p.state_out) {
+    __syncthreads();
+    store_states<kCh>(p, carry, d0, b, tid, kAll);
+  }
 }
 
-constexpr int kMaxSmem = 227 * 1024;
+template <typename K>
+cudaError_t allow_smem(K* kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+}
 
-template <typename T, int TL, int TS, int NU>
-gtr_status_t launch_scan(const SsmParams& p, int stages, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(ssm_scan_kernel<T, TL, TS, NU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  });
+template <typename T, int TL, int TS, int WC, int MB>
+gtr_status_t launch_wide(const SsmParams& p, cudaStream_t stream) {
+  static const cudaError_t attr = allow_smem(ssm_scan_wide_kernel<T, TL, TS, WC, MB>);
   if (attr != cudaSuccess) return GTR_ERR_CUDA;
-  constexpr int kCh = kWarps * 32 / TL;
-  const Layout<(int)sizeof(T), TL, TS> lay(p.N, stages);
-  return launch_serial(ssm_scan_kernel<T, TL, TS, NU>, dim3((unsigned)(p.D / kCh), (unsigned)p.B), dim3(kThreads),
-                       (size_t)lay.total, stream, p, stages);
+  constexpr int kCh = WC * 64 / TL;
+  return launch_serial(ssm_scan_wide_kernel<T, TL, TS, WC, MB>, dim3((unsigned)(p.D / kCh), (unsigned)p.B), dim3(32 * WC),
+                       (size_t)WideLayout<T, TL, TS, WC>(p.N).total, stream, p);
+}
+template <typename T, int TL, int TS, int WC, int SG, int WP>
+gtr_status_t launch_deep(const SsmParams& p, cudaStream_t stream) {
+  static const cudaError_t attr = allow_smem(ssm_scan_deep_kernel<T, TL, TS, WC, SG, WP>);
+  if (attr != cudaSuccess) return GTR_ERR_CUDA;
+  constexpr int kCh = WC * 64 / TL;
+  return launch_serial(ssm_scan_deep_kernel<T, TL, TS, WC, SG, WP>, dim3((unsigned)(p.D / kCh), (unsigned)p.B),
+                       dim3(32 * (WC * SG + WP)), (size_t)DeepLayout<T, TL, TS, WC, SG>(p.N).total, stream, p);
 }
 
+// The plan, by the number of 8-channel blocks W = B D / 8 against the 148 SMs.  Measured (bf16,
+// N = 16, 2048 positions): deep and wide<16> meet between W = 384 (4096 positions: 204 and 239
+// us) and W = 768 (211 and 142 us), at W = 576 both take 140 us; wide<8> is slower at W = 1152
+// (236 and 210 us) and faster at W = 1536 (468 and 530 us, 3840 positions).  Blocks of 4
+// channels pay while blocks of 8 leave half of the SMs idle (W = 48, 1600 positions: 24.0 and
+// 29.0 us).  Where a table over 128 positions is too large for the deep kernel (N = 64), 64 do
+// (768 channels, 1600 positions: 87 us, wide<16> 205 us).
 template <typename T>
 gtr_status_t launch_scan_t(const SsmParams& p, cudaStream_t stream) {
-  constexpr int es = (int)sizeof(T);
-  const int tiles16 = p.B * (p.D / 16);
-  if (tiles16 < 148 && Layout<es, 32, 8>(p.N, 1).total <= kMaxSmem) {
-    const int stages = Layout<es, 32, 8>(p.N, 2).total <= kMaxSmem / 2 ? 2 : 1;
-    return launch_scan<T, 32, 8, 4>(p, stages, stream);
+  const long long W = (long long)p.B * (p.D / 8);
+  if (W < 576) {
+    if (W <= 74 && DeepLayout<T, 16, 8, 1, 8>(p.N).total <= kMaxSmem) return launch_deep<T, 16, 8, 1, 8, 8>(p, stream);
+    if (DeepLayout<T, 16, 8, 2, 4>(p.N).total <= kMaxSmem) return launch_deep<T, 16, 8, 2, 4, 8>(p, stream);
+    if (DeepLayout<T, 8, 8, 1, 8>(p.N).total <= kMaxSmem) return launch_deep<T, 8, 8, 1, 8, 8>(p, stream);
   }
-  const int stages = Layout<es, 8, 16>(p.N, 2).total <= kMaxSmem / 3 ? 2 : 1;
-  return launch_scan<T, 8, 16, 1>(p, stages, stream);
+  if (W >= 1344 && p.D / p.G % 32 == 0) return launch_wide<T, 8, 8, 4, 3>(p, stream);
+  return launch_wide<T, 16, 8, 4, 3>(p, stream);
 }
 
 }  // namespace
