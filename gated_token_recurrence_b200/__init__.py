@@ -85,9 +85,14 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
+_CODES: dict = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    return {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[t.dtype]
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    return _CODES[t.dtype]
 
 
 def default_out_dtype(in_dtype):
@@ -216,54 +221,66 @@ def sswiglu_dwconv(xg, xv, conv_w, conv_b, grid: Tuple[int, int], out=None, stre
     return out
 
 
-def _on_current_device(what: str, *tensors):
+# ---------------------------------------------------------------- selective SSM, block norm
+# These calls are a few microseconds long, so the checks in front of them are written for the
+# common case: one comparison of shape, type and device per tensor, strides looked at only
+# where a tensor is not contiguous.
+def _here(t):
+    """The current device's index and its current stream's handle, for a call on tensor t."""
     import torch
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
-            raise ValueError(f"{what} takes tensors of the current CUDA device")
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _contiguous(what: str, shape, dtype, *tensors):
-    """Tensors of one shape and type (None passes), contiguous."""
-    for t in tensors:
-        if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()):
-            raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                             f"got {t.dtype} {tuple(t.shape)}")
+def _type_error(what, t, shape, dtype):
+    return ValueError(f"{what}: expected a CUDA tensor {dtype} {tuple(shape)} on the current device, "
+                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _rows(what: str, t, shape, dtype, tokens: int) -> int:
-    """The distance between the rows of consecutive tokens of a tensor whose first `tokens`
-    axes are batch and token axes; a row itself is contiguous."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    width = 1
-    for size, stride in zip(reversed(t.shape[tokens:]), reversed(t.stride()[tokens:])):
-        if size != 1 and stride != width:
-            raise ValueError(f"{what}: the values of one token must be contiguous")
-        width *= size
-    ld, behind = None, 1  # rows from one index of an axis to the next
-    for size, stride in zip(reversed(t.shape[:tokens]), reversed(t.stride()[:tokens])):
-        if size != 1:
-            if ld is None:
-                ld = stride // behind
-            if stride != ld * behind:
-                raise ValueError(f"{what}: consecutive tokens must be evenly spaced")
-        behind *= size
-    if ld is None:  # one token in all: any valid distance
-        unit = 16 // t.element_size()
-        ld = -(-width // unit) * unit
-    return ld
+def _whole(what, t, shape, dtype, dev):
+    """The address of a contiguous tensor of this shape and type (None passes)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise _type_error(what, t, shape, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    return t.data_ptr()
 
 
-def _grid_tokens(t, grid):
+def _row_distance(what, t, tokens: int) -> int:
+    """The distance between the rows of consecutive tokens of a tensor whose first `tokens` (1 or
+    2) axes are batch and token axes; a row itself (the other 1 or 2 axes) is contiguous."""
+    shape, stride = t.shape, t.stride()
+    width = shape[-1]
+    if (width != 1 and stride[-1] != 1) or (
+            len(shape) - tokens == 2 and shape[tokens] != 1 and stride[tokens] != width):
+        raise ValueError(f"{what}: the values of one token must be contiguous")
+    if shape[tokens - 1] != 1:
+        ld = stride[tokens - 1]
+        if tokens == 2 and shape[0] != 1 and stride[0] != shape[1] * ld:
+            raise ValueError(f"{what}: consecutive tokens must be evenly spaced")
+        return ld
+    if shape[0] != 1:
+        return stride[0]
+    unit = 16 // t.element_size()  # one token in all: any valid distance
+    return -(-width * (shape[tokens] if len(shape) - tokens == 2 else 1) // unit) * unit
+
+
+def _rows(what, t, shape, dtype, dev, tokens: int, width: int):
+    """(address, distance between tokens) of a tensor that may be a column range of wider rows."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise _type_error(what, t, shape, dtype)
+    return t.data_ptr(), (width if t.is_contiguous() else _row_distance(what, t, tokens))
+
+
+def _grid_of(L, grid):
     H, W = grid
-    if t.shape[1] != H * W:
-        raise ValueError(f"grid {H}x{W} does not match L={t.shape[1]}")
-    return int(H), int(W)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    if H * W != L:
+        raise ValueError(f"grid {H}x{W} does not match L={L}")
+    return H, W
 
 
 def ssm_conv(x, w, bias, grid: Tuple[int, int], direction: int = L2R, silu: bool = True, state=None,
@@ -277,38 +294,40 @@ def ssm_conv(x, w, bias, grid: Tuple[int, int], direction: int = L2R, silu: bool
     tokens of each sequence of a padded batch; outputs behind them are left as they were.
     """
     import torch
+    dev, here = _here(x)
     B, L, C = x.shape
-    H, W = _grid_tokens(x, grid)
-    K = int(w.shape[-1])
+    H, W = _grid_of(L, grid)
+    K = w.shape[-1]
+    ty, f32 = x.dtype, torch.float32
+    px, ld = _rows("x", x, (B, L, C), ty, dev, 2, C)
     if out is None:
-        out = torch.empty((B, L, C), dtype=x.dtype, device=x.device)
-    _on_current_device("ssm_conv", x, w, bias, state, state_out, lengths, out)
-    ld = _rows("ssm_conv x", x, (B, L, C), x.dtype, 2)
-    _contiguous("ssm_conv w", (C, K), torch.float32, w)
-    _contiguous("ssm_conv bias", (C,), torch.float32, bias)
-    _contiguous("ssm_conv state", (B, K - 1, C), x.dtype, state, state_out)
-    _contiguous("ssm_conv lengths", (B,), torch.int32, lengths)
-    _contiguous("ssm_conv out", (B, L, C), x.dtype, out)
-    _check(lib.gtr_ssm_conv(x.data_ptr(), ld, w.data_ptr(), _ptr(bias), _ptr(state), _ptr(state_out), _ptr(lengths),
-                            out.data_ptr(), B, H, W, C, K, int(direction), int(silu), _dtype_code(x),
-                            _stream_handle(stream)), "gtr_ssm_conv")
+        out = torch.empty((B, L, C), dtype=ty, device=x.device)
+    st = (B, K - 1, C)
+    _check(lib.gtr_ssm_conv(px, ld, _whole("w", w, (C, K), f32, dev),
+                            _whole("bias", bias, (C,), f32, dev),
+                            _whole("state", state, st, ty, dev),
+                            _whole("state_out", state_out, st, ty, dev),
+                            _whole("lengths", lengths, (B,), torch.int32, dev),
+                            _whole("out", out, (B, L, C), ty, dev), B, H, W, C, K, direction, 1 if silu else 0,
+                            _dtype_code(x), here if stream is None else stream.cuda_stream), "gtr_ssm_conv")
     return out
 
 
-def _ssm_inputs(what, u, dt, A, Bm, Cm, z, skip, dt_bias, state, state_out, lead):
+def _ssm_inputs(u, dt, A, Bm, Cm, z, skip, dt_bias, lead, dev):
     """The arguments that a scan and a step share; ``lead`` is (B, L) or (B,)."""
-    import torch
     D, N = A.shape
-    G = int(Bm.shape[-2])
-    _on_current_device(what, u, dt, A, Bm, Cm, z, skip, dt_bias, state, state_out)
-    k = len(lead)
-    ld = lambda name, t, tail: _rows(f"{what} {name}", t, (*lead, *tail), u.dtype, k)
-    _contiguous(f"{what} A", (D, N), torch.float32, A)
-    _contiguous(f"{what} skip, dt_bias", (D,), torch.float32, skip, dt_bias)
-    _contiguous(f"{what} state", (lead[0], D, N), torch.float32, state, state_out)
-    return ([u.data_ptr(), ld("u", u, (D,)), dt.data_ptr(), ld("dt", dt, (D,)), A.data_ptr(), Bm.data_ptr(),
-             ld("Bm", Bm, (G, N)), Cm.data_ptr(), ld("Cm", Cm, (G, N)), _ptr(z),
-             0 if z is None else ld("z", z, (D,)), _ptr(skip), _ptr(dt_bias)], D, N, G)
+    G = Bm.shape[-2]
+    ty, f32, k = u.dtype, A.dtype, len(lead)
+    rows, groups = (*lead, D), (*lead, G, N)
+    pu, lu = _rows("u", u, rows, ty, dev, k, D)
+    pd, ldt = _rows("dt", dt, rows, ty, dev, k, D)
+    pb, lb = _rows("Bm", Bm, groups, ty, dev, k, G * N)
+    pc, lc = _rows("Cm", Cm, groups, ty, dev, k, G * N)
+    pz, lz = (None, 0) if z is None else _rows("z", z, rows, ty, dev, k, D)
+    if _dtype_code(A) != F32:
+        raise ValueError("A: must be float32")
+    return ((pu, lu, pd, ldt, _whole("A", A, (D, N), f32, dev), pb, lb, pc, lc, pz, lz,
+             _whole("skip", skip, (D,), f32, dev), _whole("dt_bias", dt_bias, (D,), f32, dev)), D, N, G)
 
 
 def ssm_scan(u, dt, A, Bm, Cm, grid: Tuple[int, int], direction: int = L2R, skip=None, z=None, dt_bias=None,
@@ -321,16 +340,18 @@ def ssm_scan(u, dt, A, Bm, Cm, grid: Tuple[int, int], direction: int = L2R, skip
     ``state_out``, which may be ``state``.  ``lengths`` as for :func:`ssm_conv`.
     """
     import torch
+    dev, here = _here(u)
     B, L, D = u.shape
-    H, W = _grid_tokens(u, grid)
+    H, W = _grid_of(L, grid)
+    args, D, N, G = _ssm_inputs(u, dt, A, Bm, Cm, z, skip, dt_bias, (B, L), dev)
     if out is None:
         out = torch.empty((B, L, D), dtype=u.dtype, device=u.device)
-    args, D, N, G = _ssm_inputs("ssm_scan", u, dt, A, Bm, Cm, z, skip, dt_bias, state, state_out, (B, L))
-    _on_current_device("ssm_scan", lengths, out)
-    _contiguous("ssm_scan lengths", (B,), torch.int32, lengths)
-    _contiguous("ssm_scan out", (B, L, D), u.dtype, out)
-    _check(lib.gtr_ssm_scan(*args, int(softplus), _ptr(state), _ptr(state_out), _ptr(lengths), out.data_ptr(), B, H, W,
-                            D, N, G, int(direction), _dtype_code(u), _stream_handle(stream)), "gtr_ssm_scan")
+    st = (B, D, N)
+    _check(lib.gtr_ssm_scan(*args, 1 if softplus else 0, _whole("state", state, st, A.dtype, dev),
+                            _whole("state_out", state_out, st, A.dtype, dev),
+                            _whole("lengths", lengths, (B,), torch.int32, dev),
+                            _whole("out", out, (B, L, D), u.dtype, dev), B, H, W, D, N, G, direction,
+                            _dtype_code(u), here if stream is None else stream.cuda_stream), "gtr_ssm_scan")
     return out
 
 
@@ -341,16 +362,18 @@ def ssm_step(u, dt, A, Bm, Cm, state, skip=None, z=None, dt_bias=None, softplus:
     ``u``, ``dt``, ``z`` [B, D], ``Bm`` and ``Cm`` [B, G, N]; the states ``state`` [B, D, N] fp32 are
     updated in place, or written to ``state_out`` where it is given.
     """
-    import torch
+    dev, here = _here(u)
     B, D = u.shape
-    state_out = state if state_out is None else state_out
+    args, D, N, G = _ssm_inputs(u, dt, A, Bm, Cm, z, skip, dt_bias, (B,), dev)
     if out is None:
+        import torch
         out = torch.empty((B, D), dtype=u.dtype, device=u.device)
-    args, D, N, G = _ssm_inputs("ssm_step", u, dt, A, Bm, Cm, z, skip, dt_bias, state, state_out, (B,))
-    _on_current_device("ssm_step", out)
-    _contiguous("ssm_step out", (B, D), u.dtype, out)
-    _check(lib.gtr_ssm_step(*args, int(softplus), state.data_ptr(), state_out.data_ptr(), out.data_ptr(), B, D, N, G,
-                            _dtype_code(u), _stream_handle(stream)), "gtr_ssm_step")
+    st = (B, D, N)
+    ps = _whole("state", state, st, A.dtype, dev)
+    _check(lib.gtr_ssm_step(*args, 1 if softplus else 0, ps,
+                            ps if state_out is None else _whole("state_out", state_out, st, A.dtype, dev),
+                            _whole("out", out, (B, D), u.dtype, dev), B, D, N, G, _dtype_code(u),
+                            here if stream is None else stream.cuda_stream), "gtr_ssm_step")
     return out
 
 
@@ -364,22 +387,26 @@ def block_norm(y, h, post_w=None, pre_w=None, gate=None, gate_silu: bool = False
     may be ``y``.
     """
     import torch
-    B, L, C = y.shape
+    dev, here = _here(y)
+    B, L, C = rows = y.shape
+    ty, f32 = y.dtype, torch.float32
     if h_out is None:
         h_out = torch.empty_like(h)
-    if n_out is None and pre_w is not None:
+    if pre_w is None:
+        if n_out is not None:
+            raise ValueError("block_norm: n_out without pre_w")
+    elif n_out is None:
         n_out = torch.empty_like(y)
-    if pre_w is None and n_out is not None:
-        raise ValueError("block_norm: n_out without pre_w")
-    _on_current_device("block_norm", y, h, post_w, pre_w, gate, scale, h_out, n_out)
     per_token = gate is not None and gate.dim() == 3
-    _contiguous("block_norm y, n_out", (B, L, C), y.dtype, y, n_out)
-    _contiguous("block_norm h, h_out", (B, L, C), h.dtype, h, h_out)
-    _contiguous("block_norm gate", (B, L, C) if per_token else (B, C), y.dtype, gate)
-    _contiguous("block_norm post_w, pre_w, scale", (C,), torch.float32, post_w, pre_w, scale)
-    _check(lib.gtr_block_norm(y.data_ptr(), h.data_ptr(), _ptr(post_w), _ptr(pre_w), _ptr(gate), int(per_token),
-                              int(gate_silu), _ptr(scale), float(eps), h_out.data_ptr(), _ptr(n_out), B, L, C,
-                              _dtype_code(y), _dtype_code(h), _stream_handle(stream)), "gtr_block_norm")
+    _check(lib.gtr_block_norm(_whole("y", y, rows, ty, dev), _whole("h", h, rows, h.dtype, dev),
+                              _whole("post_w", post_w, (C,), f32, dev),
+                              _whole("pre_w", pre_w, (C,), f32, dev),
+                              _whole("gate", gate, rows if per_token else (B, C), ty, dev),
+                              1 if per_token else 0, 1 if gate_silu else 0,
+                              _whole("scale", scale, (C,), f32, dev), eps,
+                              _whole("h_out", h_out, rows, h.dtype, dev),
+                              _whole("n_out", n_out, rows, ty, dev), B, L, C, _dtype_code(y), _dtype_code(h),
+                              here if stream is None else stream.cuda_stream), "gtr_block_norm")
     return h_out, n_out
 
 

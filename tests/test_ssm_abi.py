@@ -82,7 +82,7 @@ def test_norm_arguments_rejected_on_host(kw, code):
 
 
 def test_row_distances_of_strided_inputs():
-    rows = lambda t, tokens=2: gtr._rows("t", t, t.shape, t.dtype, tokens)
+    rows = lambda t, tokens=2: gtr._row_distance("t", t, tokens)
     x = torch.zeros(3, 5, 64, dtype=torch.float16)
     assert rows(x) == 64 and rows(x[..., 8:40]) == 64 and rows(x[:1, :, :32]) == 64
     assert rows(x[:, :1]) == 5 * 64 and rows(x[:1, :1, :24]) == 24 and rows(x[:1, :1, :20]) == 24
