@@ -11,6 +11,7 @@
 // the gate are read once, h' and n written once.
 #include "gtr_common.cuh"
 #include "gtr_launch.cuh"
+#include "gtr_math.cuh"
 #include "gtr_vec.cuh"
 
 namespace gtr {
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) block_norm_kernel(const
       if (p.gate_rows) {
         load_row<T, kN>(gate + c, f);
 #pragma unroll
-        for (int e = 0; e < kN; ++e) fy[v][e] *= p.silu ? __fdividef(f[e], 1.f + __expf(-f[e])) : f[e];
+        for (int e = 0; e < kN; ++e) fy[v][e] *= p.silu ? silu_f32(f[e]) : f[e];
       }
       if (p.scale) {
         load_row<float, kN>(p.scale + c, f);

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "gtr_common.cuh"
+#include "gtr_math.cuh"
 #include "gtr_scan_order.cuh"
 
 namespace gtr {
@@ -28,14 +29,6 @@ struct SsmParams {
   ScanMap map;
 };
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // log(1 + exp(x)) = max(x, 0) + log1p(e) with e = exp(-|x|) in (0, 1].  Steps are small (a
 // thousandth is common), so the relative error matters: the exponential carries the rounding
 // of its argument as a first-order correction, and log1p(e) = 2 atanh(s), s = e / (2 + e) <=
@@ -46,7 +39,7 @@ __device__ __forceinline__ float softplus_f32(float x) {
   const float lo = fmaf(a, kLog2e, -hi) + a * 1.925963033500e-8f;  // log2(e) = kLog2e + 1.9259...e-8
   const float e0 = exp2_approx(hi);
   const float e = fmaf(e0, lo * 0.69314718f, e0);
-  const float s = __fdividef(e, 2.f + e);
+  const float s = e * rcp_approx(2.f + e);
   const float q = s * s;
   float t = 1.f / 13.f;
   t = fmaf(t, q, 1.f / 11.f);
@@ -56,7 +49,5 @@ __device__ __forceinline__ float softplus_f32(float x) {
   t = fmaf(t, q, 1.f / 3.f);
   return (x < 0.f ? 0.f : x) + 2.f * fmaf(s * q, t, s);  // a NaN stays one
 }
-
-__device__ __forceinline__ float ssm_silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
 
 }  // namespace gtr

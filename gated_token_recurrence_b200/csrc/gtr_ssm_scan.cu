@@ -37,24 +37,6 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, bool vali
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 r, a, b;\n\t"
-      "mov.b64 {%0, %1}, r;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-
 // Two neighbouring channels of a row.
 template <typename T> struct Pair;
 template <> struct Pair<__half> {
@@ -390,8 +372,8 @@ __global__ void __launch_bounds__(32 * WC, MB) ssm_scan_wide_kernel(const SsmPar
 #pragma unroll
       for (int i = 0; i < TS; ++i) {
         const float2 z = Pair<T>::load(hold + i * Tl::kRow);
-        ch.y[0][i] *= ssm_silu(z.x);
-        ch.y[1][i] *= ssm_silu(z.y);
+        ch.y[0][i] *= silu_f32(z.x);
+        ch.y[1][i] *= silu_f32(z.y);
       }
     }
 #pragma unroll
@@ -529,8 +511,8 @@ __global__ void __launch_bounds__(32 * (WC * SG + WP), 1) ssm_scan_deep_kernel(c
           }
           if (p.z) {
             const float2 z = Pair<T>::load(at + 2 * Tl::kRaw);
-            v.x *= ssm_silu(z.x);
-            v.y *= ssm_silu(z.y);
+            v.x *= silu_f32(z.x);
+            v.y *= silu_f32(z.y);
           }
           if (m >= 0) Pair<T>::store(static_cast<T*>(p.out) + (row0 + m) * p.D + d0 + pc, v);
         }

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kStepThreads) ssm_chain_kernel(const SsmParams
 #pragma unroll
     for (int o = LPC / 2; o > 0; o >>= 1) y += __shfl_xor_sync(mask, y, o);
     y = fmaf(skip, u, y);
-    if (p.z) y *= ssm_silu(zg);
+    if (p.z) y *= silu_f32(zg);
     if (j == 0) static_cast<T*>(p.out)[row * p.D + d] = Elem<T>::from_f32(y);
   }
   if (p.state_out) {

@@ -17,7 +17,7 @@ def _conv(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), 1), (dict(w=None), 1), (dict(out=None), 1), (dict(x=P[0] + 8), 1), (dict(out=P[4] + 8), 1),
-    (dict(si=P[3] + 8), 1), (dict(so=P[3] + 8), 1), (dict(w=P[1] + 2), 1), (dict(len=P[5] + 2), 1),
+    (dict(si=P[3] + 8), 1), (dict(so=P[3] + 8), 1), (dict(w=P[1] + 8), 1), (dict(bias=P[2] + 4), 1), (dict(len=P[5] + 2), 1),
     (dict(B=0), 1), (dict(H=0), 1), (dict(W=-1), 1), (dict(C=0), 1), (dict(K=0), 1), (dict(dir=4), 1),
     (dict(dir=-1), 1), (dict(dt=3), 1), (dict(ld=56), 1), (dict(ld=68), 1), (dict(ld=66, dt=gtr.F32), 1),
     (dict(K=1), 2), (dict(K=5), 2), (dict(C=60), 2), (dict(C=62, dt=gtr.F32), 2),
