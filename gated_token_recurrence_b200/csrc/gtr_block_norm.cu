@@ -5,10 +5,16 @@
 //     h' = h + scale * act(gate) * p                  (no scale, no gate: factor 1)
 //     n  = h' / sqrt(mean_c h'^2 + eps) * pre_w       (from h' before its rounding)
 //
-// One pass over the data: a row is held in the registers of TPR threads (a warp for rows of
-// up to 64 pieces of 16 bytes, a CTA above), the two sums of squares are reduced in fp32 with
-// shuffles, and h' never returns from memory for its norm.  Bound by HBM bandwidth: y, h and
-// the gate are read once, h' and n written once.
+// One pass over the data: a row is held in the registers of TPR threads (a warp for short rows,
+// a block above), one or two 16-byte pieces each, the two sums of squares are reduced in fp32
+// with shuffles and one barrier each, and h' never returns from memory for its norm.
+//
+// Bound by HBM bandwidth: y, h and the gate are read once, h' and n written once.  What keeps
+// loads in flight is the number of resident rows, so a thread holds little: requesting the
+// weights of the second half early, or walking over rows with weights and the next row in
+// registers, measured 20 to 60% slower on large inputs.  Measured: 30,720 rows of 1536, bf16
+// with fp32 residual, 98 us, 88% of the measured HBM bandwidth; 1600 rows of 384, fp16, 3.6 us;
+// 2441 rows of 8192, bf16 with a gate for each token, 51 us, 60%.
 #include "gtr_common.cuh"
 #include "gtr_launch.cuh"
 #include "gtr_math.cuh"
@@ -43,7 +49,7 @@ __device__ __forceinline__ void load_row(const T* p, float* f) {
 template <typename T, int N>
 __device__ __forceinline__ void store_row(T* p, const float* f) {
 #pragma unroll
-  for (int i = 0; i < N; i += Vec8<T>::N) *reinterpret_cast<uint4*>(p + i) = Vec8<T>::store(f + i);
+  for (int i = 0; i < N; i += Vec8<T>::N) __stcs(reinterpret_cast<uint4*>(p + i), Vec8<T>::store(f + i));
 }
 
 // Sum over the row's TPR threads, the same value in each of them.
@@ -52,7 +58,6 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (TPR > 32) {
-    __syncthreads();  // the previous sum has been read
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0.f;
@@ -64,10 +69,10 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 
 // T: y, gate and n; R: the residual stream; NV pieces of 16 / sizeof(T) channels a thread.
 template <typename T, typename R, int TPR, int NV>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128) block_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) block_norm_kernel(const NormParams p) {
   constexpr int kN = Vec8<T>::N;
-  constexpr int kRowsPerCta = TPR >= 128 ? 1 : 128 / TPR;
-  __shared__ float red[TPR / 32];
+  constexpr int kRowsPerCta = TPR == 32 ? 4 : 1;
+  __shared__ float red[2][TPR / 32];  // one buffer for each sum: one barrier each
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % TPR;
@@ -76,15 +81,19 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) block_norm_kernel(const
   const int nvec = p.C / kN;
   const T* y = static_cast<const T*>(p.y) + row * p.C;
   const R* h = static_cast<const R*>(p.h) + row * p.C;
+  const T* gate = static_cast<const T*>(p.gate) + (p.gate_rows == 1 ? row / p.L : row) * p.C;
   float fy[NV][kN], fh[NV][kN];
+  uint4 fg[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * TPR + lane) * kN;
 #pragma unroll
     for (int e = 0; e < kN; ++e) fy[v][e] = fh[v][e] = 0.f;
+    fg[v] = make_uint4(0, 0, 0, 0);
     if (v * TPR + lane < nvec) {
       load_row<T, kN>(y + c, fy[v]);
       load_row<R, kN>(h + c, fh[v]);
+      if (p.gate_rows) fg[v] = *reinterpret_cast<const uint4*>(gate + c);
     }
   }
   float rp = 1.f;
@@ -94,9 +103,8 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) block_norm_kernel(const
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < kN; ++e) s = fmaf(fy[v][e], fy[v][e], s);
-    rp = rsqrtf(row_sum<TPR>(s, red) / (float)p.C + p.eps);
+    rp = rsqrtf(row_sum<TPR>(s, red[0]) / (float)p.C + p.eps);
   }
-  const T* gate = static_cast<const T*>(p.gate) + (p.gate_rows == 1 ? row / p.L : row) * p.C;
   float s2 = 0.f;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -109,7 +117,7 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) block_norm_kernel(const
         for (int e = 0; e < kN; ++e) fy[v][e] *= rp * f[e];
       }
       if (p.gate_rows) {
-        load_row<T, kN>(gate + c, f);
+        Vec8<T>::load(fg[v], f);
 #pragma unroll
         for (int e = 0; e < kN; ++e) fy[v][e] *= p.silu ? silu_f32(f[e]) : f[e];
       }
@@ -127,7 +135,7 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) block_norm_kernel(const
     }
   }
   if (!p.pre_w) return;
-  const float rn = rsqrtf(row_sum<TPR>(s2, red) / (float)p.C + p.eps);
+  const float rn = rsqrtf(row_sum<TPR>(s2, red[1]) / (float)p.C + p.eps);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * TPR + lane) * kN;
@@ -143,23 +151,30 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) block_norm_kernel(const
 
 template <typename T, typename R, int TPR, int NV>
 gtr_status_t launch_norm(const NormParams& p, cudaStream_t stream) {
-  constexpr int kRowsPerCta = TPR >= 128 ? 1 : 128 / TPR;
+  constexpr int kRowsPerCta = TPR == 32 ? 4 : 1;
   const long long grid = (p.rows + kRowsPerCta - 1) / kRowsPerCta;
   if (grid > 0x7fffffffll) return GTR_ERR_UNSUPPORTED;
-  return launch_serial(block_norm_kernel<T, R, TPR, NV>, dim3((unsigned)grid), dim3(TPR > 128 ? TPR : 128), 0, stream, p);
+  return launch_serial(block_norm_kernel<T, R, TPR, NV>, dim3((unsigned)grid), dim3(TPR == 32 ? 128 : TPR), 0, stream, p);
 }
 
+// TPR by the row's pieces.  Up to 64 pieces a warp holds two a thread (54,000 rows of 384: 47 us,
+// with 64 threads and one piece 58 us), except where the rows are few and two warps a row are
+// quicker (1600 rows: 4.4 and 3.6 us); up to 256 pieces one a thread (30,720 rows of 192 pieces:
+// 98 us, two a thread 106 us); above, two: a block of half the threads waits less at its barriers.
 template <typename T, typename R>
 gtr_status_t launch_norm_c(const NormParams& p, cudaStream_t stream) {
   const int nvec = p.C / Vec8<T>::N;
   if (nvec <= 32) return launch_norm<T, R, 32, 1>(p, stream);
-  if (nvec <= 64) return launch_norm<T, R, 32, 2>(p, stream);
+  if (nvec <= 64) return p.rows <= 148 * 16 ? launch_norm<T, R, 64, 1>(p, stream) : launch_norm<T, R, 32, 2>(p, stream);
+  if (nvec <= 96) return launch_norm<T, R, 96, 1>(p, stream);
   if (nvec <= 128) return launch_norm<T, R, 128, 1>(p, stream);
-  if (nvec <= 256) return launch_norm<T, R, 128, 2>(p, stream);
+  if (nvec <= 192) return launch_norm<T, R, 192, 1>(p, stream);
+  if (nvec <= 256) return launch_norm<T, R, 256, 1>(p, stream);
+  if (nvec <= 320) return launch_norm<T, R, 160, 2>(p, stream);
+  if (nvec <= 384) return launch_norm<T, R, 192, 2>(p, stream);
   if (nvec <= 512) return launch_norm<T, R, 256, 2>(p, stream);
   if (nvec <= 1024) return launch_norm<T, R, 512, 2>(p, stream);
-  if (nvec <= 2048) return launch_norm<T, R, 512, 4>(p, stream);
-  return GTR_ERR_UNSUPPORTED;
+  return launch_norm<T, R, 512, 4>(p, stream);
 }
 
 }  // namespace

@@ -1,8 +1,6 @@
 // Host interfaces between the selective scan's files.
 #pragma once
 
-#include <cuda_runtime.h>
-
 #include "gtr.h"
 
 namespace gtr {
@@ -11,7 +9,5 @@ struct SsmParams;
 
 // Argument checks of the selective scan's calls, on the host before anything is enqueued.
 gtr_status_t validate_ssm(const SsmParams& p, int grid_H, int grid_W, int direction, int dtype);
-// One chain per channel (gtr_ssm_step.cu).
-gtr_status_t launch_ssm_chain(const SsmParams& p, int dtype, cudaStream_t stream);
 
 }  // namespace gtr
