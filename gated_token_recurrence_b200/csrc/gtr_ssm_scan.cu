@@ -15,6 +15,17 @@
 // another one.  The decays inside a lane enter products of at most TS factors; across lanes
 // and tiles one P stands for TS of them, so the approximate exponential's bias (2e-8) does
 // not build up over a long memory.
+//
+// Bound.  HBM asks for 8 bytes (16-bit data) per token and channel, 0.35 clocks an SM at the
+// measured bandwidth; N = 16 exponentials at 16 a clock and SM are 1 clock, with P, softplus
+// and SiLU 1.4; about 190 instructions at 128 a clock are 1.5, and shared memory and shuffles
+// move about 1.3.  With three resources that near one another the kernels reach about half of
+// each.  Measured (bf16, N = 16): eight 48 x 80 grids of 1536 channels 464 us (2.6 clocks a
+// token and channel on each SM; one thread per state quadruple walking the sequence took 5.07
+// ms), one 128 x 128 grid of 768 channels 272 us (20.3 ms), one 40 x 40 grid of 768 channels 31
+// us (1.15 ms).  Measured and not kept: one channel a lane (555 us: B and C are then read from
+// shared memory twice as often), sixteen positions a lane (550 us: eight warps an SM), states in
+// lanes and time in steps with two passes over time segments (700 and 245 us).
 #include "gtr_launch.cuh"
 #include "gtr_ssm.cuh"
 #include "gtr_ssm_host.h"
@@ -458,7 +469,10 @@ __global__ void __launch_bounds__(32 * (WC * SG + WP), 1) ssm_scan_deep_kernel(c
   __syncthreads();
 
   if (tid < kPrep) {
-    const int pc = 2 * (tid % (kCh / 2));  // the channels that this thread prepares and finishes
+    // the channels that this thread prepares and finishes, and their places in a tile
+    constexpr int kRows = kPrep / (kCh / 2), kIter = kTT / kRows;
+    static_assert(kTT % kRows == 0, "whole turns");
+    const int pc = 2 * (tid % (kCh / 2)), k0 = tid / (kCh / 2);
     const float2 skip = channel_pair(p.skip, d0 + pc), bias = channel_pair(p.dt_bias, d0 + pc);
     if (tiles > 0) {
       Tl::set_tokens(p, tokens, 0, len, tid, kPrep);
@@ -476,18 +490,26 @@ __global__ void __launch_bounds__(32 * (WC * SG + WP), 1) ssm_scan_deep_kernel(c
         if (more) Tl::load(p, smem + ((tile + 1) % 3) * lay.stage, tok_next, row0, d0, g, tid, kPrep);
         Tl::spread_bc(p.N, st, reinterpret_cast<float*>(smem + lay.spread + (tile & 1) * spread_bytes), tid, kPrep);
         float* delta = reinterpret_cast<float*>(smem + lay.delta + (tile & 1) * Lay::kDelta);
-#pragma unroll 2
-        for (int k = tid / (kCh / 2); k < kTT; k += kPrep / (kCh / 2)) {
-          const int r = Tl::position(k);
-          const uint8_t* at = st + Tl::raw_at(r) + pc * kES;
-          const float2 u = Pair<T>::load(at), x = Pair<T>::load(at + Tl::kRaw);
-          float e = x.x + bias.x, f = x.y + bias.y;
-          if (p.softplus) e = softplus_f32(e), f = softplus_f32(f);
-          if (tile * kTT + r >= len) e = f = 0.f;
-          delta[pc * kStride + k] = e;
-          delta[(pc + 1) * kStride + k] = f;
-          delta[(kCh + pc) * kStride + k] = e * u.x;
-          delta[(kCh + pc + 1) * kStride + k] = f * u.y;
+        float2 x[kIter], u[kIter];
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const uint8_t* at = st + Tl::raw_at(Tl::position(k0 + i * kRows)) + pc * kES;
+          u[i] = Pair<T>::load(at);
+          x[i] = add2(Pair<T>::load(at + Tl::kRaw), bias);
+        }
+        if (p.softplus) {  // one branch around them all, so that they overlap
+#pragma unroll
+          for (int i = 0; i < kIter; ++i) x[i] = make_float2(softplus_f32(x[i].x), softplus_f32(x[i].y));
+        }
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const int k = k0 + i * kRows;
+          if (tile * kTT + Tl::position(k) >= len) x[i] = make_float2(0.f, 0.f);
+          const float2 du = mul2(x[i], u[i]);
+          delta[pc * kStride + k] = x[i].x;
+          delta[(pc + 1) * kStride + k] = x[i].y;
+          delta[(kCh + pc) * kStride + k] = du.x;
+          delta[(kCh + pc + 1) * kStride + k] = du.y;
         }
         bar_arrive<kAll>(kReady + (tile & 1));
       }
@@ -497,24 +519,25 @@ __global__ void __launch_bounds__(32 * (WC * SG + WP), 1) ssm_scan_deep_kernel(c
         const int* tok = tokens + (last & 3) * kTT;
         const float* part = reinterpret_cast<const float*>(smem + lay.part + (last & 1) * Lay::kPart);
         bar_sync<kAll>(kDone + (last & 1));
-#pragma unroll 2
-        for (int k = tid / (kCh / 2); k < kTT; k += kPrep / (kCh / 2)) {
-          const int r = Tl::position(k);
-          const int m = tok[r];
-          const uint8_t* at = st + Tl::raw_at(r) + pc * kES;
-          const float2 u = Pair<T>::load(at);
-          float2 v = make_float2(skip.x * u.x, skip.y * u.y);
+        float2 v[kIter], z[kIter];
 #pragma unroll
-          for (int s = 0; s < SG; ++s) {
-            v.x += part[(s * kCh + pc) * kStride + k];
-            v.y += part[(s * kCh + pc + 1) * kStride + k];
-          }
-          if (p.z) {
-            const float2 z = Pair<T>::load(at + 2 * Tl::kRaw);
-            v.x *= silu_f32(z.x);
-            v.y *= silu_f32(z.y);
-          }
-          if (m >= 0) Pair<T>::store(static_cast<T*>(p.out) + (row0 + m) * p.D + d0 + pc, v);
+        for (int i = 0; i < kIter; ++i) {
+          const int k = k0 + i * kRows;
+          const uint8_t* at = st + Tl::raw_at(Tl::position(k)) + pc * kES;
+          z[i] = Pair<T>::load(at + 2 * Tl::kRaw);
+          v[i] = mul2(skip, Pair<T>::load(at));
+#pragma unroll
+          for (int s = 0; s < SG; ++s)
+            v[i] = add2(v[i], make_float2(part[(s * kCh + pc) * kStride + k], part[(s * kCh + pc + 1) * kStride + k]));
+        }
+        if (p.z) {
+#pragma unroll
+          for (int i = 0; i < kIter; ++i) v[i] = mul2(v[i], silu2(z[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const int m = tok[Tl::position(k0 + i * kRows)];
+          if (m >= 0) Pair<T>::store(static_cast<T*>(p.out) + (row0 + m) * p.D + d0 + pc, v[i]);
         }
       }
     }
