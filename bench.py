@@ -31,8 +31,8 @@ import torch
 ROOT = os.path.dirname(os.path.abspath(__file__))
 sys.path.insert(0, ROOT)
 
-from gtr_inputs import (DTYPES, STENCILS, WORKLOADS, make_gate_epilogue_inputs, make_inputs,  # noqa: E402
-                        make_lowrank_gate_inputs, make_stencil_inputs)
+from gtr_inputs import (DTYPES, SSM, STENCILS, WORKLOADS, make_gate_epilogue_inputs, make_inputs,  # noqa: E402
+                        make_lowrank_gate_inputs, make_ssm_inputs, make_stencil_inputs)
 
 METRIC = "GLA fwd tokens/s and % of HBM roofline at 1.6K/4.1K/16.4K tokens, 1×B200"
 L2_BYTES = 126 * 2 ** 20
@@ -394,6 +394,45 @@ def sweep_pieces(gtr, device, stream, hbm):
              {"C": st.C, "dtype": st.dtype})
         del ssets
         torch.cuda.empty_cache()
+
+    for name, w in SSM.items():  # the state space mixer: convolution, scan or one token's step
+        calls = ("step",) if w.L == 1 else ("conv", "scan")
+        n = max(3, min(16, math.ceil(3 * L2_BYTES / w.bytes_of(calls[-1]))))
+        msets = [make_ssm_inputs(w, w.index * 1000 + i, device) for i in range(n)]
+        for s in msets:
+            s["out"], s["state_out"] = torch.empty_like(s["x"]), torch.empty_like(s["state"])
+        for what in calls:
+            def mcall(i, msets=msets, w=w, what=what):
+                s = msets[i % len(msets)]
+                grid = dict(grid=(w.H, w.W), direction=i % 4, stream=stream)
+                mix = dict(skip=s["skip"], dt_bias=s["dt_bias"])
+                if what == "conv":
+                    gtr.ssm_conv(s["x"], s["conv_w"], s["conv_b"], out=s["out"], **grid)
+                elif what == "scan":
+                    gtr.ssm_scan(s["u"], s["dt"], s["A"], s["Bm"], s["Cm"], z=s["z"], out=s["out"],
+                                 state_out=s["state_out"], **mix, **grid)
+                else:
+                    one = {k: s[k][:, 0] for k in ("u", "dt", "Bm", "Cm", "z")}
+                    gtr.ssm_step(**one, A=s["A"], state=s["state"], state_out=s["state_out"], out=s["out"][:, 0],
+                                 stream=stream, **mix)
+            line(f"{name}_{what}", w.bytes_of(what), time_rotating(mcall, n, stream), w.B * w.L,
+                 {"D": w.D, "N": w.N, "dtype": w.dtype})
+        del msets
+        torch.cuda.empty_cache()
+
+    # the norms around a block at hidden width, fp32 residual stream, a gate for each sequence
+    w = SSM["ssmstack"]
+    f32 = dict(dtype=torch.float32, device=device)
+    vec = [torch.rand(w.D, **f32) + 0.5 for _ in range(3)]
+    nsets = [(torch.randn(w.B, w.L, w.D, **f32).to(DTYPES[w.dtype]), torch.randn(w.B, w.L, w.D, **f32),
+              torch.randn(w.B, w.D, **f32).to(DTYPES[w.dtype])) for _ in range(3)]
+
+    def ncall(i):
+        y, h, gate = nsets[i % 3]
+        gtr.block_norm(y, h, post_w=vec[0], pre_w=vec[1], scale=vec[2], gate=gate, h_out=nouts[i % 3][0],
+                       n_out=nouts[i % 3][1], stream=stream)
+    nouts = [(torch.empty_like(h), torch.empty_like(y)) for y, h, _ in nsets]
+    line("stack_norm", w.B * w.L * w.D * 12, time_rotating(ncall, 3, stream), w.B * w.L, {"C": w.D, "dtype": w.dtype})
     return res
 
 

@@ -308,7 +308,7 @@ def ssm_conv(x, w, bias, grid: Tuple[int, int], direction: int = L2R, silu: bool
                             _whole("state", state, st, ty, dev),
                             _whole("state_out", state_out, st, ty, dev),
                             _whole("lengths", lengths, (B,), torch.int32, dev),
-                            _whole("out", out, (B, L, C), ty, dev), B, H, W, C, K, direction, 1 if silu else 0,
+                            _whole("out", out, (B, L, C), ty, dev), B, H, W, C, K, int(direction), 1 if silu else 0,
                             _dtype_code(x), here if stream is None else stream.cuda_stream), "gtr_ssm_conv")
     return out
 
@@ -350,7 +350,7 @@ def ssm_scan(u, dt, A, Bm, Cm, grid: Tuple[int, int], direction: int = L2R, skip
     _check(lib.gtr_ssm_scan(*args, 1 if softplus else 0, _whole("state", state, st, A.dtype, dev),
                             _whole("state_out", state_out, st, A.dtype, dev),
                             _whole("lengths", lengths, (B,), torch.int32, dev),
-                            _whole("out", out, (B, L, D), u.dtype, dev), B, H, W, D, N, G, direction,
+                            _whole("out", out, (B, L, D), u.dtype, dev), B, H, W, D, N, G, int(direction),
                             _dtype_code(u), here if stream is None else stream.cuda_stream), "gtr_ssm_scan")
     return out
 

@@ -26,6 +26,8 @@
 // us (1.15 ms).  Measured and not kept: one channel a lane (555 us: B and C are then read from
 // shared memory twice as often), sixteen positions a lane (550 us: eight warps an SM), states in
 // lanes and time in steps with two passes over time segments (700 and 245 us).
+#include <atomic>
+
 #include "gtr_launch.cuh"
 #include "gtr_ssm.cuh"
 #include "gtr_ssm_host.h"
@@ -581,23 +583,31 @@ __global__ void __launch_bounds__(32 * (WC * SG + WP), 1) ssm_scan_deep_kernel(c
   }
 }
 
+// The kernel may use kMaxSmem on the current device: asked for once per device and kernel
+// (`done`, a bit for each device).
 template <typename K>
-cudaError_t allow_smem(K* kernel) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+bool allow_smem(K* kernel, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 template <typename T, int TL, int TS, int WC, int MB>
 gtr_status_t launch_wide(const SsmParams& p, cudaStream_t stream) {
-  static const cudaError_t attr = allow_smem(ssm_scan_wide_kernel<T, TL, TS, WC, MB>);
-  if (attr != cudaSuccess) return GTR_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  if (!allow_smem(ssm_scan_wide_kernel<T, TL, TS, WC, MB>, allowed)) return GTR_ERR_CUDA;
   constexpr int kCh = WC * 64 / TL;
   return launch_serial(ssm_scan_wide_kernel<T, TL, TS, WC, MB>, dim3((unsigned)(p.D / kCh), (unsigned)p.B), dim3(32 * WC),
                        (size_t)WideLayout<T, TL, TS, WC>(p.N).total, stream, p);
 }
 template <typename T, int TL, int TS, int WC, int SG, int WP>
 gtr_status_t launch_deep(const SsmParams& p, cudaStream_t stream) {
-  static const cudaError_t attr = allow_smem(ssm_scan_deep_kernel<T, TL, TS, WC, SG, WP>);
-  if (attr != cudaSuccess) return GTR_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  if (!allow_smem(ssm_scan_deep_kernel<T, TL, TS, WC, SG, WP>, allowed)) return GTR_ERR_CUDA;
   constexpr int kCh = WC * 64 / TL;
   return launch_serial(ssm_scan_deep_kernel<T, TL, TS, WC, SG, WP>, dim3((unsigned)(p.D / kCh), (unsigned)p.B),
                        dim3(32 * (WC * SG + WP)), (size_t)DeepLayout<T, TL, TS, WC, SG>(p.N).total, stream, p);

@@ -198,3 +198,64 @@ def make_stencil_inputs(s: StencilWorkload, seed: int):
     conv_w = torch.randn((s.C, 3, 3), generator=gen, dtype=torch.float32) / 3.0
     conv_b = 0.1 * torch.randn((s.C,), generator=gen, dtype=torch.float32) if s.bias else None
     return xg, xv, conv_w, conv_b
+
+
+# ----------------------------------------------------------------------------- selective SSM block
+# Recipes for the state space mixer's calls and the norms around a block: widths next to the
+# workloads above (the mixer twice the model dimension 384 or 1536 wide, 16 states).
+@dataclass(frozen=True)
+class SsmWorkload:
+    """A state space mixer over an H x W token grid (H = W = 1: one token per sequence)."""
+    name: str
+    B: int
+    H: int
+    W: int
+    D: int
+    N: int = 16
+    K: int = 4
+    dtype: str = "f16"
+    index: int = 0
+
+    @property
+    def L(self) -> int:
+        return self.H * self.W
+
+    def bytes_of(self, call: str) -> int:
+        """HBM bytes one call must move: "conv" (x, out), "scan" (u, dt, z, out, B, C; the final
+        state), "step" (the same for one token, the state in and out)."""
+        es = torch.finfo(DTYPES[self.dtype]).bits // 8
+        rows = self.B * self.L
+        if call == "conv":
+            return es * 2 * rows * self.D
+        states = (2 if call == "step" else 1) * self.B * self.D * self.N * 4
+        return es * rows * (4 * self.D + 2 * self.N) + states
+
+
+SSM = {
+    s.name: s
+    for s in [
+        SsmWorkload("ssm640", B=1, H=40, W=40, D=768, dtype="f16", index=21),
+        SsmWorkload("ssm2048", B=1, H=128, W=128, D=768, dtype="bf16", index=22),
+        SsmWorkload("ssmstack", B=8, H=48, W=80, D=1536, dtype="bf16", index=23),
+        SsmWorkload("ssmtoken", B=512, H=1, W=1, D=1536, dtype="bf16", index=24),
+    ]
+}
+
+
+def make_ssm_inputs(s: SsmWorkload, seed: int, device=None):
+    """Inputs of the mixer's calls as a dict: x, u, dt, z ~ N(0, 1) [B, L, D] and Bm, Cm ~ N(0, 1)
+    [B, L, 1, N] in the workload's dtype; conv taps ~ N(0, 1/K) [D, K] and bias 0.1 N(0, 1); decay
+    rates A = -(1 .. N) exp(0.1 N(0, 1)); dt_bias the inverse softplus of steps spread evenly in
+    the logarithm over 0.001 .. 0.1; skip 1 + 0.1 N(0, 1); state ~ N(0, 1) [B, D, N]; all of those
+    fp32."""
+    dev = device or "cpu"
+    gen = torch.Generator(device=dev).manual_seed(int(seed))
+    n = lambda *shape: torch.randn(shape, generator=gen, dtype=torch.float32, device=dev)
+    dt = DTYPES[s.dtype]
+    rows = (s.B, s.L, s.D)
+    step = torch.exp(torch.empty(s.D, device=dev).uniform_(-6.907755, -2.302585, generator=gen))
+    return dict(x=n(*rows).to(dt), u=n(*rows).to(dt), dt=n(*rows).to(dt), z=n(*rows).to(dt),
+                Bm=n(s.B, s.L, 1, s.N).to(dt), Cm=n(s.B, s.L, 1, s.N).to(dt), conv_w=n(s.D, s.K) / s.K ** 0.5,
+                conv_b=0.1 * n(s.D),
+                A=-torch.arange(1, s.N + 1, dtype=torch.float32, device=dev).repeat(s.D, 1) * torch.exp(0.1 * n(s.D, s.N)),
+                dt_bias=step + torch.log(-torch.expm1(-step)), skip=1.0 + 0.1 * n(s.D), state=n(s.B, s.D, s.N))
