@@ -1,7 +1,7 @@
 """Python binding of libgtr.so (key-only gated linear attention forward, sm_100a).
 
-Argument marshalling only: every step of the computation runs in the CUDA
-kernels of ``libgtr.so``.  PyTorch supplies device memory and streams.  There
+Argument marshalling only (ctypes; for the shortest calls the native module
+``_gtr_torch.so``): every step of the computation runs in the CUDA kernels of ``libgtr.so``.  PyTorch supplies device memory and streams.  There
 is no CPU fallback: importing this package fails if the library is missing.
 
     import gated_token_recurrence_b200 as gtr
@@ -222,58 +222,37 @@ def sswiglu_dwconv(xg, xv, conv_w, conv_b, grid: Tuple[int, int], out=None, stre
 
 
 # ---------------------------------------------------------------- selective SSM, block norm
-# These calls are a few microseconds long, so the checks in front of them are written for the
-# common case: one comparison of shape, type and device per tensor, strides looked at only
-# where a tensor is not contiguous.
-def _here(t):
-    """The current device's index and its current stream's handle, for a call on tensor t."""
+# These calls are a few microseconds long, so their tensors are looked at in native code
+# (csrc/gtr_torch.cpp): shape, type, device, strides and address of each, then the C call.
+_native = None
+
+
+def _marshal():
+    """The native marshalling module, loaded with torch at the first call."""
+    global _native
+    if _native is None:
+        import importlib.util
+        import torch  # noqa: F401  (its libraries have to be there first)
+        path = os.path.join(_HERE, "_gtr_torch.so")
+        if not os.path.exists(path):
+            raise ImportError(f"_gtr_torch.so not found at {path}; build it with "
+                              "`python gated_token_recurrence_b200/build.py`")
+        spec = importlib.util.spec_from_file_location("_gtr_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                      for n in ("gtr_ssm_conv", "gtr_ssm_scan", "gtr_ssm_step", "gtr_block_norm")))
+        _native = module
+    return _native
+
+
+def _here(t, stream):
+    """The current device and the stream of a call on tensor t."""
     import torch
     if not t.is_cuda:
         raise ValueError("expected CUDA tensors")
-    dev = torch.cuda.current_device()
-    return dev, torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _type_error(what, t, shape, dtype):
-    return ValueError(f"{what}: expected a CUDA tensor {dtype} {tuple(shape)} on the current device, "
-                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-
-
-def _whole(what, t, shape, dtype, dev):
-    """The address of a contiguous tensor of this shape and type (None passes)."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
-        raise _type_error(what, t, shape, dtype)
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: must be contiguous")
-    return t.data_ptr()
-
-
-def _row_distance(what, t, tokens: int) -> int:
-    """The distance between the rows of consecutive tokens of a tensor whose first `tokens` (1 or
-    2) axes are batch and token axes; a row itself (the other 1 or 2 axes) is contiguous."""
-    shape, stride = t.shape, t.stride()
-    width = shape[-1]
-    if (width != 1 and stride[-1] != 1) or (
-            len(shape) - tokens == 2 and shape[tokens] != 1 and stride[tokens] != width):
-        raise ValueError(f"{what}: the values of one token must be contiguous")
-    if shape[tokens - 1] != 1:
-        ld = stride[tokens - 1]
-        if tokens == 2 and shape[0] != 1 and stride[0] != shape[1] * ld:
-            raise ValueError(f"{what}: consecutive tokens must be evenly spaced")
-        return ld
-    if shape[0] != 1:
-        return stride[0]
-    unit = 16 // t.element_size()  # one token in all: any valid distance
-    return -(-width * (shape[tokens] if len(shape) - tokens == 2 else 1) // unit) * unit
-
-
-def _rows(what, t, shape, dtype, dev, tokens: int, width: int):
-    """(address, distance between tokens) of a tensor that may be a column range of wider rows."""
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
-        raise _type_error(what, t, shape, dtype)
-    return t.data_ptr(), (width if t.is_contiguous() else _row_distance(what, t, tokens))
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _grid_of(L, grid):
@@ -293,41 +272,14 @@ def ssm_conv(x, w, bias, grid: Tuple[int, int], direction: int = L2R, silu: bool
     ``state``.  For a single new token per sequence the grid is (1, 1).  ``lengths`` [B] int32:
     tokens of each sequence of a padded batch; outputs behind them are left as they were.
     """
-    import torch
-    dev, here = _here(x)
-    B, L, C = x.shape
-    H, W = _grid_of(L, grid)
-    K = w.shape[-1]
-    ty, f32 = x.dtype, torch.float32
-    px, ld = _rows("x", x, (B, L, C), ty, dev, 2, C)
+    H, W = _grid_of(x.shape[1], grid)
+    dev, here = _here(x, stream)
     if out is None:
-        out = torch.empty((B, L, C), dtype=ty, device=x.device)
-    st = (B, K - 1, C)
-    _check(lib.gtr_ssm_conv(px, ld, _whole("w", w, (C, K), f32, dev),
-                            _whole("bias", bias, (C,), f32, dev),
-                            _whole("state", state, st, ty, dev),
-                            _whole("state_out", state_out, st, ty, dev),
-                            _whole("lengths", lengths, (B,), torch.int32, dev),
-                            _whole("out", out, (B, L, C), ty, dev), B, H, W, C, K, int(direction), 1 if silu else 0,
-                            _dtype_code(x), here if stream is None else stream.cuda_stream), "gtr_ssm_conv")
+        out = x.new_empty(x.shape)
+    st = (_native or _marshal()).conv(x, w, bias, H, W, int(direction), silu, state, state_out, lengths, out, dev, here)
+    if st:
+        raise GTRError(st, "gtr_ssm_conv")
     return out
-
-
-def _ssm_inputs(u, dt, A, Bm, Cm, z, skip, dt_bias, lead, dev):
-    """The arguments that a scan and a step share; ``lead`` is (B, L) or (B,)."""
-    D, N = A.shape
-    G = Bm.shape[-2]
-    ty, f32, k = u.dtype, A.dtype, len(lead)
-    rows, groups = (*lead, D), (*lead, G, N)
-    pu, lu = _rows("u", u, rows, ty, dev, k, D)
-    pd, ldt = _rows("dt", dt, rows, ty, dev, k, D)
-    pb, lb = _rows("Bm", Bm, groups, ty, dev, k, G * N)
-    pc, lc = _rows("Cm", Cm, groups, ty, dev, k, G * N)
-    pz, lz = (None, 0) if z is None else _rows("z", z, rows, ty, dev, k, D)
-    if _dtype_code(A) != F32:
-        raise ValueError("A: must be float32")
-    return ((pu, lu, pd, ldt, _whole("A", A, (D, N), f32, dev), pb, lb, pc, lc, pz, lz,
-             _whole("skip", skip, (D,), f32, dev), _whole("dt_bias", dt_bias, (D,), f32, dev)), D, N, G)
 
 
 def ssm_scan(u, dt, A, Bm, Cm, grid: Tuple[int, int], direction: int = L2R, skip=None, z=None, dt_bias=None,
@@ -339,19 +291,14 @@ def ssm_scan(u, dt, A, Bm, Cm, grid: Tuple[int, int], direction: int = L2R, skip
     [B, D, N] fp32 is h before the first token (None: zeros); h after the last is written to
     ``state_out``, which may be ``state``.  ``lengths`` as for :func:`ssm_conv`.
     """
-    import torch
-    dev, here = _here(u)
-    B, L, D = u.shape
-    H, W = _grid_of(L, grid)
-    args, D, N, G = _ssm_inputs(u, dt, A, Bm, Cm, z, skip, dt_bias, (B, L), dev)
+    H, W = _grid_of(u.shape[1], grid)
+    dev, here = _here(u, stream)
     if out is None:
-        out = torch.empty((B, L, D), dtype=u.dtype, device=u.device)
-    st = (B, D, N)
-    _check(lib.gtr_ssm_scan(*args, 1 if softplus else 0, _whole("state", state, st, A.dtype, dev),
-                            _whole("state_out", state_out, st, A.dtype, dev),
-                            _whole("lengths", lengths, (B,), torch.int32, dev),
-                            _whole("out", out, (B, L, D), u.dtype, dev), B, H, W, D, N, G, int(direction),
-                            _dtype_code(u), here if stream is None else stream.cuda_stream), "gtr_ssm_scan")
+        out = u.new_empty(u.shape)
+    st = (_native or _marshal()).scan(u, dt, A, Bm, Cm, skip, z, dt_bias, softplus, state, state_out, lengths, out, H, W,
+                                      int(direction), dev, here)
+    if st:
+        raise GTRError(st, "gtr_ssm_scan")
     return out
 
 
@@ -362,18 +309,13 @@ def ssm_step(u, dt, A, Bm, Cm, state, skip=None, z=None, dt_bias=None, softplus:
     ``u``, ``dt``, ``z`` [B, D], ``Bm`` and ``Cm`` [B, G, N]; the states ``state`` [B, D, N] fp32 are
     updated in place, or written to ``state_out`` where it is given.
     """
-    dev, here = _here(u)
-    B, D = u.shape
-    args, D, N, G = _ssm_inputs(u, dt, A, Bm, Cm, z, skip, dt_bias, (B,), dev)
+    dev, here = _here(u, stream)
     if out is None:
-        import torch
-        out = torch.empty((B, D), dtype=u.dtype, device=u.device)
-    st = (B, D, N)
-    ps = _whole("state", state, st, A.dtype, dev)
-    _check(lib.gtr_ssm_step(*args, 1 if softplus else 0, ps,
-                            ps if state_out is None else _whole("state_out", state_out, st, A.dtype, dev),
-                            _whole("out", out, (B, D), u.dtype, dev), B, D, N, G, _dtype_code(u),
-                            here if stream is None else stream.cuda_stream), "gtr_ssm_step")
+        out = u.new_empty(u.shape)
+    st = (_native or _marshal()).step(u, dt, A, Bm, Cm, skip, z, dt_bias, softplus, state,
+                                      state if state_out is None else state_out, out, dev, here)
+    if st:
+        raise GTRError(st, "gtr_ssm_step")
     return out
 
 
@@ -386,27 +328,14 @@ def block_norm(y, h, post_w=None, pre_w=None, gate=None, gate_silu: bool = False
     [B, C] or [B, L, C]; ``post_w``, ``pre_w``, ``scale`` [C] fp32.  ``h_out`` may be ``h`` and ``n_out``
     may be ``y``.
     """
-    import torch
-    dev, here = _here(y)
-    B, L, C = rows = y.shape
-    ty, f32 = y.dtype, torch.float32
+    dev, here = _here(y, stream)
     if h_out is None:
-        h_out = torch.empty_like(h)
-    if pre_w is None:
-        if n_out is not None:
-            raise ValueError("block_norm: n_out without pre_w")
-    elif n_out is None:
-        n_out = torch.empty_like(y)
-    per_token = gate is not None and gate.dim() == 3
-    _check(lib.gtr_block_norm(_whole("y", y, rows, ty, dev), _whole("h", h, rows, h.dtype, dev),
-                              _whole("post_w", post_w, (C,), f32, dev),
-                              _whole("pre_w", pre_w, (C,), f32, dev),
-                              _whole("gate", gate, rows if per_token else (B, C), ty, dev),
-                              1 if per_token else 0, 1 if gate_silu else 0,
-                              _whole("scale", scale, (C,), f32, dev), eps,
-                              _whole("h_out", h_out, rows, h.dtype, dev),
-                              _whole("n_out", n_out, rows, ty, dev), B, L, C, _dtype_code(y), _dtype_code(h),
-                              here if stream is None else stream.cuda_stream), "gtr_block_norm")
+        h_out = h.new_empty(h.shape)
+    if n_out is None and pre_w is not None:
+        n_out = y.new_empty(y.shape)
+    st = (_native or _marshal()).norm(y, h, post_w, pre_w, gate, gate_silu, scale, eps, h_out, n_out, dev, here)
+    if st:
+        raise GTRError(st, "gtr_block_norm")
     return h_out, n_out
 
 

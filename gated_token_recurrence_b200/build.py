@@ -1,4 +1,5 @@
-"""Build libgtr.so in-tree with nvcc for sm_100a (B200).
+"""Build libgtr.so in-tree with nvcc for sm_100a (B200), and _gtr_torch.so, the argument
+marshalling of the state space calls for torch tensors, with g++.
 
 Usage: ``python gated_token_recurrence_b200/build.py [--force] [--verbose] [--ptxas]``
 (run as a script: importing the package itself needs the built library).
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgtr.so")
+TORCH_LIB = os.path.join(HERE, "_gtr_torch.so")
+TORCH_SRC = os.path.join(CSRC, "gtr_torch.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -44,8 +47,31 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_torch_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/gtr_torch.cpp against the installed torch's headers."""
+    deps = [TORCH_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(TORCH_LIB) and all(os.path.getmtime(d) <= os.path.getmtime(TORCH_LIB) for d in deps):
+        return TORCH_LIB
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), TORCH_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    done = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if done.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + done.stdout.decode(errors="replace"))
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_report: bool = False) -> str:
     """Compile every csrc/*.cu into libgtr.so (objects in csrc/_build, linked with cudart static)."""
+    build_torch_binding(force, verbose)
     if not force and not _stale():
         return LIB
     objdir = os.path.join(CSRC, "_build")

@@ -82,7 +82,7 @@ def test_norm_arguments_rejected_on_host(kw, code):
 
 
 def test_row_distances_of_strided_inputs():
-    rows = lambda t, tokens=2: gtr._row_distance("t", t, tokens)
+    rows = lambda t, tokens=2: gtr._marshal().distance(t, tokens)
     x = torch.zeros(3, 5, 64, dtype=torch.float16)
     assert rows(x) == 64 and rows(x[..., 8:40]) == 64 and rows(x[:1, :, :32]) == 64
     assert rows(x[:, :1]) == 5 * 64 and rows(x[:1, :1, :24]) == 24 and rows(x[:1, :1, :20]) == 24
@@ -91,6 +91,23 @@ def test_row_distances_of_strided_inputs():
     for bad in (x[:, :4], x.transpose(0, 1), x[..., ::2], bc.transpose(-1, -2)[:, :, 0]):
         with pytest.raises(ValueError):
             rows(bad)
+
+
+def test_marshalling_refuses_what_it_cannot_pass():
+    """Each refusal is a ValueError that names the argument; nothing reaches the library."""
+    m = gtr._marshal()
+    x, w = torch.zeros(1, 4, 64), torch.zeros(64, 4)
+    args = lambda **kw: tuple({**dict(x=x, w=w, bias=None, H=2, W=2, d=0, silu=True, st=None, so=None, ln=None, out=x, dev=0,
+                                      stream=0), **kw}.values())
+    for kw, word in ((dict(), "x: expected a CUDA tensor"), (dict(x=None), "x: expected a tensor"),
+                     (dict(x=torch.zeros(4, 64)), "x: expected 3 axes"), (dict(w=torch.zeros(64)), "w: expected 2 axes"),
+                     (dict(x=x.double()), "x: must be float32, float16 or bfloat16")):
+        with pytest.raises(ValueError, match=word):
+            m.conv(*args(**kw))
+    with pytest.raises(ValueError):
+        m.conv(x)
+    with pytest.raises(TypeError):
+        m.conv(*args(dev="0"))
 
 
 def test_host_tensors_are_refused():
