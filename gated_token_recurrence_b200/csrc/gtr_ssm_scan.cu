@@ -20,7 +20,7 @@
 // measured bandwidth; N = 16 exponentials at 16 a clock and SM are 1 clock, with P, softplus
 // and SiLU 1.4; about 190 instructions at 128 a clock are 1.5, and shared memory and shuffles
 // move about 1.3.  With three resources that near one another the kernels reach about half of
-// each.  Measured (bf16, N = 16): eight 48 x 80 grids of 1536 channels 464 us (2.6 clocks a
+// each.  Measured (bf16, N = 16): eight 48 x 80 grids of 1536 channels 462 us (2.6 clocks a
 // token and channel on each SM; one thread per state quadruple walking the sequence took 5.07
 // ms), one 128 x 128 grid of 768 channels 272 us (20.3 ms), one 40 x 40 grid of 768 channels 31
 // us (1.15 ms).  Measured and not kept: one channel a lane (555 us: B and C are then read from
@@ -207,10 +207,10 @@ struct Chains {
     for (int s = 1; s < TL; s *= 2) {
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        const float hp = __shfl_up_sync(0xffffffffu, h[v], s, TL);
+        const float hp = __shfl_up_sync(0xffffffffu, h[v], s * (32 / TL));
         if (tl >= s) h[v] = fmaf(P[v], hp, h[v]);
         if (2 * s < TL) {
-          const float Pp = __shfl_up_sync(0xffffffffu, P[v], s, TL);
+          const float Pp = __shfl_up_sync(0xffffffffu, P[v], s * (32 / TL));
           if (tl >= s) P[v] *= Pp;
         }
       }
@@ -218,7 +218,7 @@ struct Chains {
     float x[2];
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      const float hp = __shfl_up_sync(0xffffffffu, h[v], 1, TL);
+      const float hp = __shfl_up_sync(0xffffffffu, h[v], 32 / TL);
       x[v] = tl > 0 ? hp : in[v];
     }
 #pragma unroll
@@ -319,8 +319,10 @@ __global__ void __launch_bounds__(32 * WC, MB) ssm_scan_wide_kernel(const SsmPar
   float* a_table = reinterpret_cast<float*>(smem + lay.table);
   float* carry = a_table + p.N * kCh;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int tl = lane % TL;
-  const int c = ((tid >> 5) * (32 / TL) + lane / TL) * 2;  // the first of this lane's channels
+  // lanes of one time lane are neighbours: their 16-byte reads of B and C are the same, and the
+  // shared memory answers them in half the time that it takes for repeats eight lanes apart
+  const int tl = lane / (32 / TL);
+  const int c = ((tid >> 5) * (32 / TL) + lane % (32 / TL)) * 2;  // the first of this lane's channels
   const int d0 = blockIdx.x * kCh, b = blockIdx.y;
   const int g = d0 / (p.D / p.G);
   const long long row0 = (long long)b * p.L;
@@ -421,7 +423,8 @@ template <typename T, int TL, int TS, int WC, int SG>
 struct DeepLayout {
   static constexpr int kCh = WC * 64 / TL;
   using Tl = Tile<T, TL, TS, kCh>;
-  static constexpr int kStride = Tl::kTT + 4;  // of one channel: a warp's channels on other banks
+  // of one channel: the channels that eight lanes read 16 bytes of at once are on other banks
+  static constexpr int kStride = Tl::kTT + (TL == 16 ? 8 : 4);
   static constexpr int kDelta = 2 * kCh * kStride * 4;  // delta and delta u
   static constexpr int kPart = SG * kCh * kStride * 4;
   int stage, spread, delta, part, tokens, table, total;  // [3] raw stages at 0
@@ -545,8 +548,8 @@ __global__ void __launch_bounds__(32 * (WC * SG + WP), 1) ssm_scan_deep_kernel(c
     }
   } else {
     const int lane = tid & 31, warp = (tid - kPrep) >> 5;
-    const int tl = lane % TL;
-    const int c = ((warp % WC) * (32 / TL) + lane / TL) * 2;
+    const int tl = lane / (32 / TL);
+    const int c = ((warp % WC) * (32 / TL) + lane % (32 / TL)) * 2;
     const int sg = warp / WC;
     for (int tile = 0; tile < tiles; ++tile) {
       bar_sync<kAll>(kReady + (tile & 1));
@@ -614,12 +617,17 @@ gtr_status_t launch_deep(const SsmParams& p, cudaStream_t stream) {
 }
 
 // The plan, by the number of 8-channel blocks W = B D / 8 against the 148 SMs.  Measured (bf16,
-// N = 16, 2048 positions): deep and wide<16> meet between W = 384 (4096 positions: 204 and 239
-// us) and W = 768 (211 and 142 us), at W = 576 both take 140 us; wide<8> is slower at W = 1152
-// (236 and 210 us) and faster at W = 1536 (468 and 530 us, 3840 positions).  Blocks of 4
-// channels pay while blocks of 8 leave half of the SMs idle (W = 48, 1600 positions: 24.0 and
-// 29.0 us).  Where a table over 128 positions is too large for the deep kernel (N = 64), 64 do
-// (768 channels, 1600 positions: 87 us, wide<16> 205 us).
+// N = 16, 2048 positions unless noted):
+//   deep and wide<16> take 141 and 139 us at W = 576 and meet between W = 384 (4096 positions:
+//   206 and 234 us) and W = 768 (214 and 139 us);
+//   wide<16> holds three blocks an SM, one wave up to W = 888; wide<8> with sixteen positions a
+//   lane two of twice its channels, one wave up to W = 1184 (W = 1152: 206, 164 us; W = 768: 139,
+//   163 us); wide<8> with eight positions is quicker from there on (W = 1536, 3840 positions: 462
+//   us, sixteen positions 502, wide<16> 519; W = 1152: 233 us);
+//   blocks of 4 channels pay while blocks of 8 leave half of the SMs idle (W = 48, 1600
+//   positions: 22.8 and 29.6 us);
+//   where a table over 128 positions is too large for the deep kernel (N = 64), 64 do (768
+//   channels, 1600 positions: 87 us, wide<16> 205 us).
 template <typename T>
 gtr_status_t launch_scan_t(const SsmParams& p, cudaStream_t stream) {
   const long long W = (long long)p.B * (p.D / 8);
@@ -628,7 +636,10 @@ gtr_status_t launch_scan_t(const SsmParams& p, cudaStream_t stream) {
     if (DeepLayout<T, 16, 8, 2, 4>(p.N).total <= kMaxSmem) return launch_deep<T, 16, 8, 2, 4, 8>(p, stream);
     if (DeepLayout<T, 8, 8, 1, 8>(p.N).total <= kMaxSmem) return launch_deep<T, 8, 8, 1, 8, 8>(p, stream);
   }
-  if (W >= 1344 && p.D / p.G % 32 == 0) return launch_wide<T, 8, 8, 4, 3>(p, stream);
+  if (p.D / p.G % 32 == 0) {
+    if (W > 888 && W <= 1184 && WideLayout<T, 8, 16, 4>(p.N).total <= kMaxSmem / 2) return launch_wide<T, 8, 16, 4, 2>(p, stream);
+    if (W >= 1344) return launch_wide<T, 8, 8, 4, 3>(p, stream);
+  }
   return launch_wide<T, 16, 8, 4, 3>(p, stream);
 }
 

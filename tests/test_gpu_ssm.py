@@ -182,7 +182,8 @@ def test_scan_widths(B, D):
     check_scan("f16", B, 5, 53, D, 8, 1, direction=1)
 
 
-@pytest.mark.parametrize("dtype,B,D,N,G", [("bf16", 12, 1056, 16, 1), ("f32", 11, 1056, 16, 3), ("bf16", 2, 768, 64, 2),
+@pytest.mark.parametrize("dtype,B,D,N,G", [("bf16", 12, 1056, 16, 1), ("f16", 8, 1024, 16, 2),
+                                           ("f32", 8, 1024, 48, 1), ("f32", 11, 1056, 16, 3), ("bf16", 2, 768, 64, 2),
                                            ("f32", 1, 800, 64, 1), ("f32", 5, 1040, 64, 1), ("f16", 1, 768, 48, 1)])
 def test_scan_plans_with_more_states(dtype, B, D, N, G):
     check_scan(dtype, B, 3, 50, D, N, G, direction=2, lengths=[150, 77] + [149] * (B - 2) if B > 1 else None)
