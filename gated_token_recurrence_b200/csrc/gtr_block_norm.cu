@@ -13,7 +13,7 @@
 // loads in flight is the number of resident rows, so a thread holds little: requesting the
 // weights of the second half early, or walking over rows with weights and the next row in
 // registers, measured 20 to 60% slower on large inputs.  Measured: 30,720 rows of 1536, bf16
-// with fp32 residual, 98 us, 88% of the measured HBM bandwidth; 1600 rows of 384, fp16, 3.6 us;
+// with fp32 residual, 98 us, 88% of the measured HBM bandwidth; 1600 rows of 384, fp16, 3.0 us;
 // 2441 rows of 8192, bf16 with a gate for each token, 51 us, 60%.
 #include "gtr_common.cuh"
 #include "gtr_launch.cuh"
@@ -73,7 +73,6 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) block_norm_kernel(const
   constexpr int kN = Vec8<T>::N;
   constexpr int kRowsPerCta = TPR == 32 ? 4 : 1;
   __shared__ float red[2][TPR / 32];  // one buffer for each sum: one barrier each
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % TPR;
   const long long row = (long long)blockIdx.x * kRowsPerCta + threadIdx.x / TPR;

@@ -23,7 +23,10 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 // Launch with programmatic stream serialisation: the kernel may start while its predecessor
 // in the stream drains, and waits for it (griddepcontrol.wait) before its first access to
-// global memory.  Every thread of such a kernel executes that wait, also those that then
+// global memory.  These kernels do not let their own successors start early
+// (griddepcontrol.launch_dependents): blocks that wait on the SMs take the places of blocks that
+// would run, and are packed on the SMs that have room first (one token's convolution 3.3 us with
+// it, 2.3 us without; a norm of 1600 rows 3.6 and 3.0 us).  Every thread of such a kernel executes that wait, also those that then
 // have nothing to do: a kernel that ended without it could end before its predecessor, and
 // its successor would wait for the wrong one.
 template <typename... KArgs, typename... Args>

@@ -12,7 +12,7 @@
 //
 // Bound: HBM, 2 elements of traffic for 2 K + 5 operations.  Measured (bf16, K = 4, SiLU): eight
 // 48 x 80 grids of 1152 channels 33 us, 65% of the measured HBM bandwidth (without SiLU's two
-// special functions per element 30 us); one 40 x 40 grid of 768 channels 4.6 us.  It was 54 and
+// special functions per element 30 us); one 40 x 40 grid of 768 channels 4.0 us.  It was 54 and
 // 12 us with taps read from global memory by each thread and strips of 8 and 4 positions.
 #include "gtr_common.cuh"
 #include "gtr_launch.cuh"
@@ -48,7 +48,6 @@ template <typename T, int K>
 __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(const ConvParams p) {
   constexpr int kN = Vec8<T>::N;
   __shared__ uint4 ring[kDepth][kConvThreads];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const unsigned idx = blockIdx.x * (unsigned)kConvThreads + threadIdx.x;
   const unsigned row = idx / p.nvec, vec = idx - row * p.nvec;

@@ -22,9 +22,9 @@
 // move about 1.3.  With three resources that near one another the kernels reach about half of
 // each.  Measured (bf16, N = 16): eight 48 x 80 grids of 1536 channels 462 us (2.6 clocks a
 // token and channel on each SM; one thread per state quadruple walking the sequence took 5.07
-// ms), one 128 x 128 grid of 768 channels 272 us (20.3 ms), one 40 x 40 grid of 768 channels 31
-// us (1.15 ms).  Measured and not kept: one channel a lane (555 us: B and C are then read from
-// shared memory twice as often), sixteen positions a lane (550 us: eight warps an SM), states in
+// ms), one 128 x 128 grid of 768 channels 275 us (20.3 ms), one 40 x 40 grid of 768 channels 31
+// us (1.15 ms), two 64 x 64 grids of 1536 channels 171 us.  Measured and not kept: one channel a lane (555 us: B and C are then read from
+// shared memory twice as often), sixteen positions a lane on the first of these (502 us: eight warps an SM in two waves), states in
 // lanes and time in steps with two passes over time segments (700 and 245 us).
 #include <atomic>
 
@@ -37,7 +37,8 @@
 namespace gtr {
 namespace {
 
-constexpr int kMaxSmem = 227 * 1024;
+constexpr int kMaxSmem = 227 * 1024;  // of a block; an SM has 1 KB more and keeps 1 KB of each block
+constexpr int kSms = 148;
 
 // Copy `BYTES` (8 or 16) to shared memory asynchronously, or fill with zeros.
 template <int BYTES>
@@ -327,7 +328,6 @@ __global__ void __launch_bounds__(32 * WC, MB) ssm_scan_wide_kernel(const SsmPar
   const int g = d0 / (p.D / p.G);
   const long long row0 = (long long)b * p.L;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int len = sequence_length(p, b), tiles = (len + kTT - 1) / kTT;
   load_tables<kCh>(p, a_table, carry, d0, b, tid, kThreads);
@@ -467,7 +467,6 @@ __global__ void __launch_bounds__(32 * (WC * SG + WP), 1) ssm_scan_deep_kernel(c
   const long long row0 = (long long)b * p.L;
   const int spread_bytes = Tl::spread(p.N);
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int len = sequence_length(p, b), tiles = (len + kTT - 1) / kTT;
   load_tables<kCh>(p, a_table, carry, d0, b, tid, kAll);
@@ -604,8 +603,15 @@ gtr_status_t launch_wide(const SsmParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> allowed{0};
   if (!allow_smem(ssm_scan_wide_kernel<T, TL, TS, WC, MB>, allowed)) return GTR_ERR_CUDA;
   constexpr int kCh = WC * 64 / TL;
+  // Blocks that leave room on the SMs are spread evenly by asking for as much shared memory as
+  // lets no SM take more than its share: next to blocks of a kernel that still runs they would
+  // be packed on part of the SMs (144 blocks of <32, 8> then took the time of 432, 84 us, and 50
+  // us when spread)
+  const int need = WideLayout<T, TL, TS, WC>(p.N).total;
+  const long long share = ((long long)p.B * (p.D / kCh) + kSms - 1) / kSms;
+  const int even = share <= MB ? (kMaxSmem + 1024) / (int)share - 1024 : 0;
   return launch_serial(ssm_scan_wide_kernel<T, TL, TS, WC, MB>, dim3((unsigned)(p.D / kCh), (unsigned)p.B), dim3(32 * WC),
-                       (size_t)WideLayout<T, TL, TS, WC>(p.N).total, stream, p);
+                       (size_t)(need > even ? need : even), stream, p);
 }
 template <typename T, int TL, int TS, int WC, int SG, int WP>
 gtr_status_t launch_deep(const SsmParams& p, cudaStream_t stream) {
@@ -616,31 +622,71 @@ gtr_status_t launch_deep(const SsmParams& p, cudaStream_t stream) {
                        dim3(32 * (WC * SG + WP)), (size_t)DeepLayout<T, TL, TS, WC, SG>(p.N).total, stream, p);
 }
 
-// The plan, by the number of 8-channel blocks W = B D / 8 against the 148 SMs.  Measured (bf16,
-// N = 16, 2048 positions unless noted):
-//   deep and wide<16> take 141 and 139 us at W = 576 and meet between W = 384 (4096 positions:
-//   206 and 234 us) and W = 768 (214 and 139 us);
-//   wide<16> holds three blocks an SM, one wave up to W = 888; wide<8> with sixteen positions a
-//   lane two of twice its channels, one wave up to W = 1184 (W = 1152: 206, 164 us; W = 768: 139,
-//   163 us); wide<8> with eight positions is quicker from there on (W = 1536, 3840 positions: 462
-//   us, sixteen positions 502, wide<16> 519; W = 1152: 233 us);
-//   blocks of 4 channels pay while blocks of 8 leave half of the SMs idle (W = 48, 1600
-//   positions: 22.8 and 29.6 us);
-//   where a table over 128 positions is too large for the deep kernel (N = 64), 64 do (768
-//   channels, 1600 positions: 87 us, wide<16> 205 us).
+// The plan.  Each kernel holds a number of blocks on an SM, and one that has some left over for
+// another wave pays for it whole, so the plans are compared by what their waves take: `one` and
+// `most` are the measured microseconds of 2048 positions (bf16, N = 16) with one block on each
+// SM and with as many as it holds; in between they are taken as evenly spaced, and everything
+// scales with the positions, whole tiles of them, and with N but for a share (two sequences of
+// 4096 positions and 768 channels, N = 64: deep<8> over 64 positions 420 us, wide<16, 8> 499 us).
+// Measured with the plan taken and the next best (2048 positions each, B D / 8 = W):
+//   W = 144  deep 36, wide<32, 8> 50;            W = 288  wide<32, 8> 67, wide<16, 16> 69, deep 72
+//   W = 432  wide<32, 8> 86, wide<16, 16> 91;    W = 576  wide<16, 16> 92, wide<16, 8> 106
+//   W = 880  wide<16, 8> 139, wide<16, 16> 154;  W = 1152 wide<8, 16> 164, wide<16, 16> 182
+//   W = 1728 wide<8, 8> 247, wide<8, 16> 268
+// The lengths of a padded batch are on the device; its blocks are counted half, as if the
+// lengths were spread evenly (three sequences of 416 channels, one full, one of some tokens, one
+// empty: deep 27 us, a plan for all of them at once 56 us).
+struct ScanPlan {
+  int channels, positions;  // of a block's tile
+  int holds;                // blocks on an SM where shared memory allows it
+  float one, most;
+  float fixed;              // share of that which does not grow with N
+};
+enum { kDeep4, kDeep8, kDeep8Short, kWide32x8, kWide16x16, kWide16x8, kWide8x16, kWide8x8, kPlans };
+constexpr ScanPlan kScanPlans[kPlans] = {
+    {4, 128, 1, 28.f, 28.f, .36f},   {8, 128, 1, 36.f, 36.f, .36f},  {8, 64, 1, 41.f, 41.f, .48f},
+    {8, 256, 3, 50.f, 86.f, .29f},   {16, 256, 2, 69.f, 91.f, .29f}, {16, 128, 3, 80.f, 139.f, .29f},
+    {32, 128, 2, 116.f, 163.f, .29f}, {32, 64, 3, 139.f, 247.f, .29f},
+};
+
+float plan_cost(const SsmParams& p, int plan, int smem) {
+  constexpr float kNever = 3e38f;
+  const ScanPlan& s = kScanPlans[plan];
+  const int fits = (kMaxSmem + 1024) / (smem + 1024);  
+  if (smem > kMaxSmem || p.D / p.G % s.channels != 0) return kNever;
+  const int holds = fits < s.holds ? fits : s.holds;
+  const auto wave = [&](long long blocks) {  // microseconds with so many blocks on an SM
+    return blocks == 0 ? 0.f : s.one + (s.holds > 1 ? (s.most - s.one) * (float)(blocks - 1) / (float)(s.holds - 1) : 0.f);
+  };
+  const long long all = (long long)p.B * (p.D / s.channels), blocks = p.lengths ? (all + 1) / 2 : all;
+  const long long slots = (long long)kSms * holds;
+  const long long tiles = ((long long)p.L + s.positions - 1) / s.positions;
+  return ((float)(blocks / slots) * wave(holds) + wave((blocks % slots + kSms - 1) / kSms)) *
+         (s.fixed + (1.f - s.fixed) * (float)p.N / 16.f) * (float)(tiles * s.positions);
+}
+
 template <typename T>
 gtr_status_t launch_scan_t(const SsmParams& p, cudaStream_t stream) {
-  const long long W = (long long)p.B * (p.D / 8);
-  if (W < 576) {
-    if (W <= 74 && DeepLayout<T, 16, 8, 1, 8>(p.N).total <= kMaxSmem) return launch_deep<T, 16, 8, 1, 8, 8>(p, stream);
-    if (DeepLayout<T, 16, 8, 2, 4>(p.N).total <= kMaxSmem) return launch_deep<T, 16, 8, 2, 4, 8>(p, stream);
-    if (DeepLayout<T, 8, 8, 1, 8>(p.N).total <= kMaxSmem) return launch_deep<T, 8, 8, 1, 8, 8>(p, stream);
+  const int smem[kPlans] = {DeepLayout<T, 16, 8, 1, 8>(p.N).total, DeepLayout<T, 16, 8, 2, 4>(p.N).total,
+                            DeepLayout<T, 8, 8, 1, 8>(p.N).total,  WideLayout<T, 32, 8, 4>(p.N).total,
+                            WideLayout<T, 16, 16, 4>(p.N).total,   WideLayout<T, 16, 8, 4>(p.N).total,
+                            WideLayout<T, 8, 16, 4>(p.N).total,    WideLayout<T, 8, 8, 4>(p.N).total};
+  int best = kWide16x8;  // fits for every N and type
+  float least = plan_cost(p, best, smem[best]);
+  for (int i = 0; i < kPlans; ++i) {
+    const float c = plan_cost(p, i, smem[i]);
+    if (c < least) best = i, least = c;
   }
-  if (p.D / p.G % 32 == 0) {
-    if (W > 888 && W <= 1184 && WideLayout<T, 8, 16, 4>(p.N).total <= kMaxSmem / 2) return launch_wide<T, 8, 16, 4, 2>(p, stream);
-    if (W >= 1344) return launch_wide<T, 8, 8, 4, 3>(p, stream);
+  switch (best) {
+    case kDeep4: return launch_deep<T, 16, 8, 1, 8, 8>(p, stream);
+    case kDeep8: return launch_deep<T, 16, 8, 2, 4, 8>(p, stream);
+    case kDeep8Short: return launch_deep<T, 8, 8, 1, 8, 8>(p, stream);
+    case kWide32x8: return launch_wide<T, 32, 8, 4, 3>(p, stream);
+    case kWide16x16: return launch_wide<T, 16, 16, 4, 2>(p, stream);
+    case kWide8x16: return launch_wide<T, 8, 16, 4, 2>(p, stream);
+    case kWide8x8: return launch_wide<T, 8, 8, 4, 3>(p, stream);
+    default: return launch_wide<T, 16, 8, 4, 3>(p, stream);
   }
-  return launch_wide<T, 16, 8, 4, 3>(p, stream);
 }
 
 }  // namespace

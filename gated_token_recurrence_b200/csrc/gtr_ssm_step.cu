@@ -36,7 +36,6 @@ __device__ __forceinline__ float transposed_sum(float (&v)[LPC], int j) {
 template <typename T, int LPC, int NV, int R>
 __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmParams p) {
   static_assert(R == LPC || R == 1, "");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int j = threadIdx.x % LPC;
   const int d = blockIdx.x * (kStepThreads / LPC) + threadIdx.x / LPC;
