@@ -328,3 +328,68 @@ def test_calls_are_bitwise_repeatable():
     g = on_gpu(c)
     a = gtr.ssm_scan(**g, grid=(16, 40))
     assert all(torch.equal(a, gtr.ssm_scan(**g, grid=(16, 40))) for _ in range(3))
+
+
+def test_two_streams_at_once():
+    """Calls of every kind on two streams at the same time give what they give alone."""
+    def work(seed):
+        c = scan_case("bf16", 2, 16, 40, 160, 16, 1, seed=seed)
+        g = on_gpu(c)
+        gen = torch.Generator().manual_seed(seed)
+        w = rnd(gen, 160, 4).cuda()
+
+        def run():
+            u = gtr.ssm_conv(g["z"], w, None, grid=(16, 40), direction=1)
+            h = torch.empty_like(g["state"])
+            rest = {k: v for k, v in g.items() if k != "u"}
+            y = gtr.ssm_scan(u, **rest, grid=(16, 40), direction=1, state_out=h)
+            one = {k: g[k][:, 0] for k in ("dt", "Bm", "Cm", "z")}
+            s = gtr.ssm_step(u[:, 0], A=g["A"], state=h, skip=g["skip"], dt_bias=g["dt_bias"], **one)
+            return u, y, h, s, *gtr.block_norm(y, u, pre_w=g["skip"])
+        return run
+    runs = [work(1), work(2)]
+    alone = [r() for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        both = []
+        for s, r in zip(streams, runs):
+            with torch.cuda.stream(s):
+                both.append(r())
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_stream_argument():
+    c = scan_case("f32", 1, 1, 40, 32, 8, 1)
+    g = on_gpu(c)
+    ref = gtr.ssm_scan(**g, grid=(1, 40))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.zeros_like(ref)
+    torch.cuda.synchronize()
+    gtr.ssm_scan(**g, grid=(1, 40), out=out, stream=s)
+    s.synchronize()
+    assert torch.equal(out, ref)
+
+
+def test_refusals_on_the_gpu():
+    """Wrong types, shapes, spacings and overlaps are errors that leave nothing enqueued."""
+    c = scan_case("f16", 1, 2, 4, 32, 8, 1)
+    g = on_gpu(c)
+    for bad in (dict(u=g["u"].float()), dict(A=g["A"].half()), dict(Bm=g["Bm"][:, :4]), dict(z=g["z"].cpu()),
+                dict(state=g["state"][:, :16]), dict(lengths=torch.ones(1, device="cuda")),
+                dict(out=torch.empty(1, 8, 64, dtype=torch.float16, device="cuda")[..., ::2])):
+        with pytest.raises(ValueError):
+            gtr.ssm_scan(**{**g, **bad}, grid=(2, 4))
+    for bad in (dict(out=g["u"]), dict(state_out=g["A"].view(1, 32, 8)), dict(direction=4)):
+        with pytest.raises(gtr.GTRError):
+            gtr.ssm_scan(**{**g, **bad}, grid=(2, 4))
+    with pytest.raises(ValueError):
+        gtr.ssm_scan(**g, grid=(2, 5))
+    with pytest.raises(ValueError):
+        gtr.block_norm(g["u"], g["u"], gate=g["z"][:, :3])
+    with pytest.raises(gtr.GTRError):
+        gtr.block_norm(g["u"], g["u"], n_out=torch.empty_like(g["u"]))
+    torch.cuda.synchronize()
