@@ -283,8 +283,8 @@ gtr_status_t gtr_sswiglu_dwconv(const void *xg, const void *xv, const float *con
  * block; the pages of the GTR paper have no counterpart.  Like the rest of the library they
  * are forward only.  Rules that they share:
  *
- *   - all pointers are device pointers of the current device; data pointers are 16-byte
- *     aligned, pointers to per-channel vectors and lengths 4-byte (gtr_block_norm: 16);
+ *   - all pointers are device pointers of the current device, 16-byte aligned; skip, dt_bias
+ *     and lengths need only 4 bytes;
  *   - asynchronous on `stream`, no workspace, no allocation, no synchronisation; capturable;
  *     calls on different streams and captured graphs are independent of one another;
  *   - `*_ld` is the distance, in elements, between the rows of consecutive tokens m (and of
@@ -309,7 +309,7 @@ gtr_status_t gtr_sswiglu_dwconv(const void *xg, const void *xv, const float *con
  * and act = SiLU where `silu` is not 0, else the identity.  Prompts and single tokens alike:
  * for one new token per sequence the grid is 1 x 1 and state_in = state_out is its cache.
  *   x [B, L, C] rows x_ld apart, out [B, L, C], in `dtype`
- *   w [C, K] fp32, 16-byte aligned, K = 2, 3 or 4 (otherwise GTR_ERR_UNSUPPORTED);  bias [C] fp32 or NULL
+ *   w [C, K] fp32, K = 2, 3 or 4 (otherwise GTR_ERR_UNSUPPORTED);  bias [C] fp32 or NULL
  *   state_in [B, K-1, C] in `dtype`: the inputs of the K-1 positions before the first, oldest
  *     first (NULL: zeros);  state_out, the same layout: the last K-1 inputs (NULL: not
  *     wanted; may be state_in)
