@@ -20,10 +20,10 @@
 // measured bandwidth; N = 16 exponentials at 16 a clock and SM are 1 clock, with P, softplus
 // and SiLU 1.4; about 190 instructions at 128 a clock are 1.5, and shared memory and shuffles
 // move about 1.3.  With three resources that near one another the kernels reach about half of
-// each.  Measured (bf16, N = 16): eight 48 x 80 grids of 1536 channels 462 us (2.6 clocks a
+// each.  Measured (bf16, N = 16): eight 48 x 80 grids of 1536 channels 455 us (2.5 clocks a
 // token and channel on each SM; one thread per state quadruple walking the sequence took 5.07
-// ms), one 128 x 128 grid of 768 channels 275 us (20.3 ms), one 40 x 40 grid of 768 channels 31
-// us (1.15 ms), two 64 x 64 grids of 1536 channels 171 us.  Measured and not kept: one channel
+// ms), one 128 x 128 grid of 768 channels 273 us (20.3 ms), one 40 x 40 grid of 768 channels 31
+// us (1.15 ms), two 64 x 64 grids of 1536 channels 170 us.  Measured and not kept: one channel
 // a lane (555 us on the first of these: B and C are then read from shared memory twice as
 // often), states in lanes and time in steps with two passes over time segments (700 us on the
 // first, 245 us on the second).
