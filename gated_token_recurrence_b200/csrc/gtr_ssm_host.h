@@ -1,6 +1,8 @@
 // Host interfaces between the selective scan's files.
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include "gtr.h"
 
 namespace gtr {
@@ -9,5 +11,7 @@ struct SsmParams;
 
 // Argument checks of the selective scan's calls, on the host before anything is enqueued.
 gtr_status_t validate_ssm(const SsmParams& p, int grid_H, int grid_W, int direction, int dtype);
+// A scan of a few tokens for many channels (gtr_ssm_step.cu).
+gtr_status_t launch_ssm_walk(const SsmParams& p, int dtype, cudaStream_t stream);
 
 }  // namespace gtr

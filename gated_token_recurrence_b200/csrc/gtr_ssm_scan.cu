@@ -666,6 +666,16 @@ float plan_cost(const SsmParams& p, int plan, int smem) {
          (s.fixed + (1.f - s.fixed) * (float)p.N / 16.f) * (float)(tiles * s.positions);
 }
 
+// Prompts that leave a tile mostly empty walk token by token instead (gtr_ssm_step.cu).  Measured
+// (bf16, N = 16, 1536 channels), walk and tiles: 512 sequences of 4 tokens 77 and 500 us, of 24
+// 376 and 505 us; 16 sequences of 4 tokens 4.3 and 19.9 us, of 12 10.1 and 20.0 us; 4 sequences of
+// 4 tokens 3.8 and 8.4 us, of 12 8.9 and 8.4 us; one sequence of 4 tokens, 768 channels: 3.6 and
+// 3.5 us.
+bool few_tokens(const SsmParams& p) {
+  const long long channels = (long long)p.B * p.D;
+  return channels >= 16384 ? p.L <= 24 : channels >= 4096 && p.L <= 8;
+}
+
 template <typename T>
 gtr_status_t launch_scan_t(const SsmParams& p, cudaStream_t stream) {
   const int smem[kPlans] = {DeepLayout<T, 16, 8, 1, 8>(p.N).total, DeepLayout<T, 16, 8, 2, 4>(p.N).total,
@@ -708,6 +718,7 @@ extern "C" gtr_status_t gtr_ssm_scan(const void* u, int64_t u_ld, const void* dt
   p.L = grid_H * grid_W;
   p.map = ScanMap::make(direction, grid_H, grid_W);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (few_tokens(p)) return launch_ssm_walk(p, dtype, s);
   switch (dtype) {
     case GTR_F16: return launch_scan_t<__half>(p, s);
     case GTR_BF16: return launch_scan_t<__nv_bfloat16>(p, s);

@@ -182,6 +182,16 @@ def test_scan_widths(B, D):
     check_scan("f16", B, 5, 53, D, 8, 1, direction=1)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,D,N,G,grid", [(16, 1024, 16, 1, (1, 1)), (17, 1024, 8, 2, (4, 6)), (33, 512, 24, 1, (3, 5)),
+                                          (5, 1024, 64, 2, (2, 4)), (16, 1024, 40, 1, (5, 5)), (64, 272, 32, 1, (24, 1))])
+def test_scan_of_a_few_tokens(dtype, B, D, N, G, grid):
+    """Short prompts on many channels walk token by token up to 24 (8) positions."""
+    L = grid[0] * grid[1]
+    for kw in (dict(), dict(strided=True, lengths=[(3 * i) % (L + 2) - 1 for i in range(B)], in_place=True)):
+        check_scan(dtype, B, *grid, D, N, G, direction=3, **kw)
+
+
 @pytest.mark.parametrize("dtype,B,D,N,G", [("bf16", 12, 1056, 16, 1), ("f16", 8, 1024, 16, 2),
                                            ("f32", 8, 1024, 48, 1), ("f32", 11, 1056, 16, 3), ("bf16", 2, 768, 64, 2),
                                            ("f32", 1, 800, 64, 1), ("f32", 5, 1040, 64, 1), ("f16", 1, 768, 48, 1)])
