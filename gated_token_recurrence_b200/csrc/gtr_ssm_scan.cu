@@ -27,6 +27,8 @@
 // a lane (555 us on the first of these: B and C are then read from shared memory twice as
 // often), states in lanes and time in steps with two passes over time segments (700 us on the
 // first, 245 us on the second).
+#include <float.h>
+
 #include <atomic>
 
 #include "gtr_launch.cuh"
@@ -268,13 +270,21 @@ struct Chains {
   }
 };
 
+// A log2(e), held finite.  A rate of -inf, or one that the factor takes out of fp32's range, forgets
+// at once either way, but the positions behind a sequence's end in its last tile have steps of 0
+// and must keep the state: exp2(0 * -inf) would be a NaN.  A NaN stays one.
+__device__ __forceinline__ float log2_rate(float a) {
+  const float r = a * kLog2e;
+  return fabsf(r) > FLT_MAX ? copysignf(FLT_MAX, r) : r;
+}
+
 // The tables that live as long as the block, [N][CH]: A log2(e) and the carried states.
 template <int CH>
 __device__ __forceinline__ void load_tables(const SsmParams& p, float* a_table, float* carry, int d0, int b, int tid,
                                             int threads) {
   for (int i = tid; i < p.N * CH; i += threads) {
     const int ch = i / p.N, n = i - ch * p.N;
-    a_table[n * CH + ch] = __ldg(p.A + (long long)(d0 + ch) * p.N + n) * kLog2e;
+    a_table[n * CH + ch] = log2_rate(__ldg(p.A + (long long)(d0 + ch) * p.N + n));
     carry[n * CH + ch] = p.state_in ? p.state_in[((long long)b * p.D + d0 + ch) * p.N + n] : 0.f;
   }
 }

@@ -16,6 +16,9 @@ namespace gtr {
 namespace {
 
 constexpr int kStepThreads = 128;
+// The exponent delta A log2(e) as (2 delta) (A log2(e) / 2): the same bits, and every finite rate
+// stays finite, so that a step of 0 keeps the state (0 * -inf would be a NaN).
+constexpr float kHalfLog2e = 0.5f * kLog2e;
 
 // Sums over the LPC lanes of a channel of LPC values each; lane j gets the sum of value j.
 template <int LPC>
@@ -64,12 +67,13 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmParams 
     if (p.softplus) dl = softplus_f32(dl);
   }
   const float du = dl * u;
+  dl *= 2.f;  // kHalfLog2e's other half
   float2 A[NV][2];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p.A + (long long)d * p.N + 4 * (v * LPC + j)));
-    A[v][0] = make_float2(a.x * kLog2e, a.y * kLog2e);
-    A[v][1] = make_float2(a.z * kLog2e, a.w * kLog2e);
+    A[v][0] = make_float2(a.x * kHalfLog2e, a.y * kHalfLog2e);
+    A[v][1] = make_float2(a.z * kHalfLog2e, a.w * kHalfLog2e);
   }
   const T* bm_row = static_cast<const T*>(p.Bm) + b0 * p.bm_ld + g * p.N + 4 * j;
   const T* cm_row = static_cast<const T*>(p.Cm) + b0 * p.cm_ld + g * p.N + 4 * j;
@@ -139,8 +143,8 @@ __global__ void __launch_bounds__(kStepThreads) ssm_walk_kernel(const SsmParams 
     const float4 a = __ldg(reinterpret_cast<const float4*>(p.A + (long long)d * p.N + 4 * (v * LPC + j)));
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.state_in) s = __ldcs(reinterpret_cast<const float4*>(p.state_in + state + 4 * LPC * v));
-    A[v][0] = make_float2(a.x * kLog2e, a.y * kLog2e);
-    A[v][1] = make_float2(a.z * kLog2e, a.w * kLog2e);
+    A[v][0] = make_float2(a.x * kHalfLog2e, a.y * kHalfLog2e);
+    A[v][1] = make_float2(a.z * kHalfLog2e, a.w * kHalfLog2e);
     h[v][0] = make_float2(s.x, s.y);
     h[v][1] = make_float2(s.z, s.w);
   }
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kStepThreads) ssm_walk_kernel(const SsmParams 
     const float z = p.z ? Elem<T>::to_f32(static_cast<const T*>(p.z)[row * p.z_ld + d]) : 0.f;
     if (p.softplus) dl = softplus_f32(dl);
     const float du = dl * u;
-    const float2 dl2 = make_float2(dl, dl), du2 = make_float2(du, du);
+    const float2 dl2 = make_float2(2.f * dl, 2.f * dl), du2 = make_float2(du, du);
     const T* bm_row = static_cast<const T*>(p.Bm) + row * p.bm_ld + g * p.N + 4 * j;
     const T* cm_row = static_cast<const T*>(p.Cm) + row * p.cm_ld + g * p.N + 4 * j;
     float2 acc = make_float2(0.f, 0.f);

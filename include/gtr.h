@@ -329,7 +329,8 @@ gtr_status_t gtr_ssm_conv(const void *x, int64_t x_ld, const float *w, const flo
  *   u, dt, z [B, L, D] rows u_ld, dt_ld, z_ld apart, out [B, L, D], in `dtype`; z NULL: no gate
  *   Bm, Cm [B, L, G, N] in `dtype`, rows bm_ld, cm_ld apart (the G * N values of a token
  *     contiguous)
- *   A [D, N] fp32, delta * A <= 0 (not checked);  skip, dt_bias [D] fp32 or NULL (0)
+ *   A [D, N] fp32, delta * A <= 0 (not checked; a step of 0 keeps the state at every finite rate,
+ *     a rate of -inf forgets at every step above 0);  skip, dt_bias [D] fp32 or NULL (0)
  *   state_in [B, D, N] fp32: h before the first position (NULL: zeros);  state_out: h after
  *     the last (NULL: not wanted; may be state_in)
  *   N a multiple of 8 up to 64;  D / G a multiple of 16;  B <= 65535; otherwise

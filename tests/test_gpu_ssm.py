@@ -403,3 +403,37 @@ def test_refusals_on_the_gpu():
     with pytest.raises(gtr.GTRError):
         gtr.block_norm(g["u"], g["u"], n_out=torch.empty_like(g["u"]))
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------- rates beyond fp32
+@pytest.mark.parametrize("rate", [float("-inf"), -3e38])
+@pytest.mark.parametrize("B,D,L,lengths", [(1, 32, 1, None), (1, 32, 130, None), (2, 768, 130, [77, 130]),
+                                           (5, 1200, 130, None), (40, 272, 70, None), (16, 1024, 8, None)])
+def test_scan_with_rates_at_the_end_of_the_range(rate, B, D, L, lengths):
+    """A state whose rate is -inf, or leaves fp32's range once multiplied by log2(e), forgets at
+    once; the positions behind a sequence's end, which lie in its last tile, leave it alone.  Every
+    exp(delta A) is 0 here, as for the rate -1e30 that the oracle gets."""
+    c = scan_case("f32", B, 1, L, D, 16, 1)
+    c["A"][:, 3] = -1e30
+    ref, st, oerr, serr = oracle.ssm_scan(**c, H=1, W=L, lengths=lengths, rounding=ROUNDING)
+    c["A"][:, 3] = rate
+    out = torch.full((B, L, D), SENTINEL, device="cuda")
+    so = torch.full((B, D, 16), SENTINEL, device="cuda")
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    gtr.ssm_scan(**on_gpu(c), grid=(1, L), lengths=ln, out=out, state_out=so)
+    within(out, ref, oerr + half_step("f32", ref), "out")
+    within(so, st, serr + half_step("f32", st), "state")
+
+
+@pytest.mark.parametrize("B,L", [(2, 1), (2, 40), (16, 8)])
+def test_a_step_of_zero_keeps_the_state_at_any_rate(B, L):
+    c = scan_case("f32", B, 1, L, 1024, 16, 1, bias=False)
+    c["dt"][:] = -200.0
+    c["A"][:, 5] = -3e38
+    g = on_gpu(c)
+    so = torch.empty_like(g["state"])
+    gtr.ssm_scan(**g, grid=(1, L), state_out=so)
+    assert torch.equal(so, g["state"])
+    one = {k: g[k][:, 0] for k in ("u", "dt", "Bm", "Cm", "z")}
+    gtr.ssm_step(**one, A=g["A"], state=g["state"], skip=g["skip"], state_out=so.zero_())
+    assert torch.equal(so, g["state"])
