@@ -224,6 +224,12 @@ extern "C" gtr_status_t gtr_ssm_conv(const void* x, int64_t x_ld, const float* w
   if (overlaps(out, no, x, nx) || overlaps(out, no, state_in, ns) || overlaps(out, no, state_out, ns) ||
       overlaps(state_out, ns, x, nx) || (state_in != state_out && overlaps(state_in, ns, state_out, ns)))
     return GTR_ERR_INVALID_ARG;
+  const struct {
+    const void* q;
+    size_t n;
+  } params[] = {{w, (size_t)C * K * 4}, {bias, (size_t)C * 4}, {lengths, (size_t)B * 4}};
+  for (const auto& i : params)
+    if (overlaps(out, no, i.q, i.n) || overlaps(state_out, ns, i.q, i.n)) return GTR_ERR_INVALID_ARG;
   ConvParams p{x, x_ld, w, bias, state_in, state_out, lengths, out, B, (int)L, C, silu != 0, 0, 0, 0, 0,
                ScanMap::make(direction, grid_H, grid_W)};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -119,3 +119,25 @@ def test_host_tensors_are_refused():
         gtr.block_norm(x, x)
     with pytest.raises(ValueError):
         gtr.ssm_conv(x, torch.zeros(64, 4), v, grid=(2, 3))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=P[1]), dict(out=P[1] + 64 * 4 * 4 - 16), dict(out=P[2]), dict(out=P[2] + 64 * 4 - 16), dict(len=P[4]),
+    dict(len=P[4] + 2 * 3 * 5 * 64 * 2 - 4), dict(len=P[4] - 4), dict(so=P[1]), dict(so=P[1] + 64 * 4 * 4 - 16),
+    dict(so=P[2]), dict(so=P[2] + 64 * 4 - 16), dict(si=P[5], len=P[3]), dict(si=P[5], len=P[3] + 2 * 3 * 64 * 2 - 4)])
+def test_conv_outputs_over_weights_or_lengths_are_rejected(kw):
+    """The first and the last bytes of the taps, the bias and the lengths under an output."""
+    assert _conv(**kw) == 1
+
+
+def test_conv_outputs_next_to_weights_or_lengths_pass_the_overlap_checks():
+    """So many tokens that the call ends with GTR_ERR_UNSUPPORTED after the overlap checks."""
+    x, out, B, H = 1 << 44, 1 << 45, 50, 1 << 14
+    behind = out + B * H * H * 64 * 2
+    many = dict(B=B, H=H, W=H, x=x, out=out)
+    for kw in (dict(w=behind), dict(w=out - 64 * 4 * 4), dict(bias=behind), dict(bias=out - 64 * 4), dict(len=behind),
+               dict(len=out - B * 4)):
+        assert _conv(**many, **kw) == 2
+    for kw in (dict(w=behind - 16), dict(w=out - 64 * 4 * 4 + 16), dict(bias=behind - 16), dict(bias=out - 64 * 4 + 16),
+               dict(len=behind - 4), dict(len=out - B * 4 + 4)):
+        assert _conv(**many, **kw) == 1
