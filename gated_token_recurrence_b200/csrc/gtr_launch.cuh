@@ -21,6 +21,13 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// A runtime call that failed.  The runtime also keeps the error for whoever asks for the last one:
+// it is taken out, or the next call that asks would report it as its own.
+inline gtr_status_t cuda_failed() {
+  (void)cudaGetLastError();
+  return GTR_ERR_CUDA;
+}
+
 // Launch with programmatic stream serialisation: the kernel may start while its predecessor
 // in the stream drains, and waits for it (griddepcontrol.wait) before its first access to
 // global memory.  These kernels do not let their own successors start early
@@ -42,7 +49,8 @@ gtr_status_t launch_serial(void (*kernel)(KArgs...), dim3 grid, dim3 block, size
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...) == cudaSuccess ? GTR_OK : GTR_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...) == cudaSuccess ? GTR_OK
+                                                                                         : cuda_failed();
 }
 
 }  // namespace gtr

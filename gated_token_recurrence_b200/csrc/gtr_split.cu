@@ -316,6 +316,7 @@ gtr_status_t launch_split_typed(const Problem& p, const SplitWorkspace& ws, cuda
   }
   const int Nc = p.n_chunks();
   const dim3 grid(Nc, p.heads, p.B);
+  (void)cudaGetLastError();  // an earlier call's error is not this one's
   split_summary_kernel<Tin><<<grid, 256, kSummarySmem, stream>>>(p, ws.U, ws.a_last);
   split_scan_kernel<<<dim3(p.B * p.heads, (kD * kD) / 256), 256, 0, stream>>>(ws.U, ws.a_last, ws.S, Nc);
   split_output_kernel<Tin, Tout><<<grid, 256, kOutputSmem, stream>>>(p, ws.S);

@@ -612,7 +612,7 @@ bool allow_smem(K* kernel, std::atomic<unsigned long long>& done) {
 template <typename T, int TL, int TS, int WC, int MB>
 gtr_status_t launch_wide(const SsmParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> allowed{0};
-  if (!allow_smem(ssm_scan_wide_kernel<T, TL, TS, WC, MB>, allowed)) return GTR_ERR_CUDA;
+  if (!allow_smem(ssm_scan_wide_kernel<T, TL, TS, WC, MB>, allowed)) return cuda_failed();
   constexpr int kCh = WC * 64 / TL;
   // Blocks that leave room on the SMs are spread evenly by asking for as much shared memory as
   // lets no SM take more than its share: next to blocks of a kernel that still runs they would
@@ -627,7 +627,7 @@ gtr_status_t launch_wide(const SsmParams& p, cudaStream_t stream) {
 template <typename T, int TL, int TS, int WC, int SG, int WP>
 gtr_status_t launch_deep(const SsmParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> allowed{0};
-  if (!allow_smem(ssm_scan_deep_kernel<T, TL, TS, WC, SG, WP>, allowed)) return GTR_ERR_CUDA;
+  if (!allow_smem(ssm_scan_deep_kernel<T, TL, TS, WC, SG, WP>, allowed)) return cuda_failed();
   constexpr int kCh = WC * 64 / TL;
   return launch_serial(ssm_scan_deep_kernel<T, TL, TS, WC, SG, WP>, dim3((unsigned)(p.D / kCh), (unsigned)p.B),
                        dim3(32 * (WC * SG + WP)), (size_t)DeepLayout<T, TL, TS, WC, SG>(p.N).total, stream, p);

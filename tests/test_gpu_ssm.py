@@ -437,3 +437,37 @@ def test_a_step_of_zero_keeps_the_state_at_any_rate(B, L):
     one = {k: g[k][:, 0] for k in ("u", "dt", "Bm", "Cm", "z")}
     gtr.ssm_step(**one, A=g["A"], state=g["state"], skip=g["skip"], state_out=so.zero_())
     assert torch.equal(so, g["state"])
+
+
+def test_a_refused_launch_leaves_no_error_behind():
+    """Calls on a stream whose capture has become invalid are errors; the next call elsewhere is
+    not, whichever it is: the split GLA path looks at the runtime's last error."""
+    q, lg = torch.randn(1, 64, 1, 64, device="cuda"), -torch.rand(1, 64, 1, 64, device="cuda")
+    ws = gtr.new_workspace(1, 1, 8, 8, 64, 64, gtr.F32, "split", device="cuda")
+    split = lambda: gtr.gla_fwd(q, q, q, lg, grid=(8, 8), path="split", workspace=ws)
+    ref = split()
+    c = scan_case("f32", 1, 1, 40, 32, 8, 1)
+    g = on_gpu(c)
+    w, ones, buf, so = torch.ones(32, 4, device="cuda"), torch.ones(32, device="cuda"), torch.empty_like(g["u"]), \
+        torch.empty_like(g["state"])
+    one = {k: g[k][:, 0] for k in ("u", "dt", "Bm", "Cm", "z")}
+    rest = {k: g[k] for k in ("A", "skip", "dt_bias")}
+    calls = [lambda: gtr.ssm_conv(g["u"], w, None, grid=(1, 40), out=buf),
+             lambda: gtr.ssm_scan(**g, grid=(1, 40), out=buf, state_out=so),
+             lambda: gtr.ssm_step(**one, **rest, state=g["state"], state_out=so, out=buf[:, 0]),
+             lambda: gtr.block_norm(g["u"], g["z"], pre_w=ones, h_out=buf, n_out=torch.empty_like(buf))]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    for call in calls:
+        refused = False
+        with pytest.raises(RuntimeError):  # the capture itself ends with an error
+            with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=torch.cuda.Stream()):
+                with pytest.raises(RuntimeError):
+                    torch.cuda.synchronize()  # not permitted while capturing
+                try:
+                    call()
+                except gtr.GTRError as e:
+                    refused = e.status == 3
+        assert refused
+        assert torch.equal(split(), ref)
