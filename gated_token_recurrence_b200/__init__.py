@@ -9,9 +9,15 @@ is no CPU fallback: importing this package fails if the library is missing.
 
 Tensors are [B, L, heads, d] (log_gamma fp32 [B, L, heads, d_k]), contiguous,
 on the current CUDA device.  See include/gtr.h for the full contract.
+
+``stream`` (None: the current one) is the stream that a call runs on.  It must already wait for
+whatever writes the inputs.  A result that the call allocates comes from that stream's memory
+pool: before another stream reads it, it waits for ``stream``, and ``record_stream`` keeps it for
+work there that outlives it.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -113,6 +119,15 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _empty(like, shape, stream, dtype=None):
+    """Memory for a result of a call on ``stream``, from that stream's pool."""
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return _empty(like, shape, None, dtype)
+    return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+
+
 def _shape(q, v, grid):
     B, L, heads, d_k = q.shape
     H, W = grid
@@ -147,7 +162,7 @@ def gla_fwd(q, k, v, log_gamma, grid: Tuple[int, int], direction: int = L2R, out
     import torch
     B, heads, H, W, d_k, d_v = _shape(q, v, grid)
     if out is None:
-        out = torch.empty((B, H * W, heads, d_v), dtype=default_out_dtype(q.dtype), device=q.device)
+        out = _empty(q, (B, H * W, heads, d_v), stream, default_out_dtype(q.dtype))
     for t in (q, k, v, log_gamma, out):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("gla_fwd takes contiguous CUDA tensors")
@@ -162,7 +177,10 @@ def gla_fwd(q, k, v, log_gamma, grid: Tuple[int, int], direction: int = L2R, out
         _check(lib.gtr_gla_fwd(*args, s), "gtr_gla_fwd")
     else:
         if workspace is None:
-            workspace = new_workspace(B, heads, H, W, d_k, d_v, _dtype_code(q), path, q.device)
+            # zeroed on the stream that uses it
+            n = max(256, workspace_bytes(B, heads, H, W, d_k, d_v, _dtype_code(q), path))
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                workspace = q.new_zeros((n,), dtype=torch.uint8)
         _check(lib.gtr_gla_fwd_ex(*args, PATHS[path], workspace.data_ptr(), workspace.numel(), s),
                "gtr_gla_fwd_ex")
     return out
@@ -182,7 +200,7 @@ def gla_block_fwd(q, k, v, grid: Tuple[int, int], direction: int = L2R, log_gamm
     import torch
     B, heads, H, W, d_k, d_v = _shape(q, v, grid)
     if out is None:
-        out = torch.empty((B, H * W, heads, d_v), dtype=default_out_dtype(q.dtype), device=q.device)
+        out = _empty(q, (B, H * W, heads, d_v), stream, default_out_dtype(q.dtype))
     tensors = [t for t in (q, k, v, log_gamma, gate_z, gate_w2, gate_b, out_gate, norm_w, out) if t is not None]
     for t in tensors:
         if not t.is_cuda or not t.is_contiguous():
@@ -210,7 +228,7 @@ def sswiglu_dwconv(xg, xv, conv_w, conv_b, grid: Tuple[int, int], out=None, stre
     if H * W != L or xg.shape != xv.shape or xg.dtype != xv.dtype:
         raise ValueError("xg and xv must both be [B, H*W, C] of one dtype")
     if out is None:
-        out = torch.empty_like(xv)
+        out = _empty(xv, xv.shape, stream)
     for t in (xg, xv, conv_w, out) + (() if conv_b is None else (conv_b,)):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("sswiglu_dwconv takes contiguous CUDA tensors")
@@ -275,7 +293,7 @@ def ssm_conv(x, w, bias, grid: Tuple[int, int], direction: int = L2R, silu: bool
     H, W = _grid_of(x.shape[1], grid)
     dev, here = _here(x, stream)
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _empty(x, x.shape, stream)
     st = (_native or _marshal()).conv(x, w, bias, H, W, int(direction), silu, state, state_out, lengths, out, dev, here)
     if st:
         raise GTRError(st, "gtr_ssm_conv")
@@ -294,7 +312,7 @@ def ssm_scan(u, dt, A, Bm, Cm, grid: Tuple[int, int], direction: int = L2R, skip
     H, W = _grid_of(u.shape[1], grid)
     dev, here = _here(u, stream)
     if out is None:
-        out = u.new_empty(u.shape)
+        out = _empty(u, u.shape, stream)
     st = (_native or _marshal()).scan(u, dt, A, Bm, Cm, skip, z, dt_bias, softplus, state, state_out, lengths, out, H, W,
                                       int(direction), dev, here)
     if st:
@@ -311,7 +329,7 @@ def ssm_step(u, dt, A, Bm, Cm, state, skip=None, z=None, dt_bias=None, softplus:
     """
     dev, here = _here(u, stream)
     if out is None:
-        out = u.new_empty(u.shape)
+        out = _empty(u, u.shape, stream)
     st = (_native or _marshal()).step(u, dt, A, Bm, Cm, skip, z, dt_bias, softplus, state,
                                       state if state_out is None else state_out, out, dev, here)
     if st:
@@ -330,9 +348,9 @@ def block_norm(y, h, post_w=None, pre_w=None, gate=None, gate_silu: bool = False
     """
     dev, here = _here(y, stream)
     if h_out is None:
-        h_out = h.new_empty(h.shape)
+        h_out = _empty(h, h.shape, stream)
     if n_out is None and pre_w is not None:
-        n_out = y.new_empty(y.shape)
+        n_out = _empty(y, y.shape, stream)
     st = (_native or _marshal()).norm(y, h, post_w, pre_w, gate, gate_silu, scale, eps, h_out, n_out, dev, here)
     if st:
         raise GTRError(st, "gtr_block_norm")
