@@ -250,7 +250,8 @@ def _marshal():
     global _native
     if _native is None:
         import importlib.util
-        import torch  # noqa: F401  (its libraries have to be there first)
+        import sysconfig
+        import torch  # its libraries have to be there first
         path = os.path.join(_HERE, "_gtr_torch.so")
         if not os.path.exists(path):
             raise ImportError(f"_gtr_torch.so not found at {path}; build it with "
@@ -258,6 +259,11 @@ def _marshal():
         spec = importlib.util.spec_from_file_location("_gtr_torch", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
+        here = f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"
+        built_for = getattr(module, "built_for", "something older")
+        if built_for != here:
+            raise ImportError(f"{path} was built for {built_for}, this is {here}; build it again with "
+                              "`python gated_token_recurrence_b200/build.py`")
         module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                       for n in ("gtr_ssm_conv", "gtr_ssm_scan", "gtr_ssm_step", "gtr_block_norm")))
         _native = module

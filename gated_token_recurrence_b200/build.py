@@ -1,5 +1,5 @@
-"""Build libgtr.so in-tree with nvcc for sm_100a (B200), and _gtr_torch.so, the argument
-marshalling of the state space calls for torch tensors, with g++.
+"""Build libgtr.so in-tree with nvcc for sm_100a (B200), and, where torch is installed,
+_gtr_torch.so, the argument marshalling of the state space calls for torch tensors, with g++.
 
 Usage: ``python gated_token_recurrence_b200/build.py [--force] [--verbose] [--ptxas]``
 (run as a script: importing the package itself needs the built library).
@@ -20,6 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgtr.so")
 TORCH_LIB = os.path.join(HERE, "_gtr_torch.so")
 TORCH_SRC = os.path.join(CSRC, "gtr_torch.cpp")
+OBJDIR = os.path.join(CSRC, "_build")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -47,17 +48,51 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build_torch_binding(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/gtr_torch.cpp against the installed torch's headers."""
+def _torch_binding_obstacle():
+    """What keeps the marshalling module from being built here, or None."""
+    import shutil
+    import sysconfig
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return "torch is not installed"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h is not installed"
+    if shutil.which("g++") is None:
+        return "g++ is not installed"
+    return None
+
+
+def torch_binding_target() -> str:
+    """What the module is compiled for: it is loaded and kept for exactly this."""
+    import sysconfig
+    import torch
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
+def build_torch_binding(force: bool = False, verbose: bool = False):
+    """Compile csrc/gtr_torch.cpp against the installed torch's headers.  Where torch, the Python
+    headers or g++ are missing it only says so: the C-ABI library does not need the module."""
     deps = [TORCH_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(TORCH_LIB) and all(os.path.getmtime(d) <= os.path.getmtime(TORCH_LIB) for d in deps):
+    stamp = os.path.join(OBJDIR, "_gtr_torch.target")  # what the module beside it was compiled for
+    fresh = os.path.exists(TORCH_LIB) and all(os.path.getmtime(d) <= os.path.getmtime(TORCH_LIB) for d in deps)
+    obstacle = _torch_binding_obstacle()
+    if obstacle is not None:
+        if (force or not fresh) and os.path.exists(TORCH_LIB):
+            os.remove(TORCH_LIB)  # made for another gtr.h
+        print(f"_gtr_torch.so not built: {obstacle}; the state space and block norm calls of the Python "
+              "binding need it", file=sys.stderr)
+        return None
+    target = torch_binding_target()
+    if not force and fresh and os.path.exists(stamp) and open(stamp).read() == target:
         return TORCH_LIB
     import sysconfig
     import torch
     root = os.path.dirname(torch.__file__)
     tmp = TORCH_LIB + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           f'-DGTR_BUILT_FOR="{target}"', "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), TORCH_SRC, "-o", tmp,
            "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
@@ -66,20 +101,27 @@ def build_torch_binding(force: bool = False, verbose: bool = False) -> str:
     if done.returncode != 0:
         raise RuntimeError("g++ failed:\n" + done.stdout.decode(errors="replace"))
     os.replace(tmp, TORCH_LIB)
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(target)
     return TORCH_LIB
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_report: bool = False) -> str:
-    """Compile every csrc/*.cu into libgtr.so (objects in csrc/_build, linked with cudart static)."""
+    """Compile every csrc/*.cu into libgtr.so (objects in csrc/_build, linked with cudart static),
+    then the binding's module where torch is installed."""
+    if force or _stale():
+        _build_library(verbose, ptxas_report)
     build_torch_binding(force, verbose)
-    if not force and not _stale():
-        return LIB
-    objdir = os.path.join(CSRC, "_build")
-    os.makedirs(objdir, exist_ok=True)
+    return LIB
+
+
+def _build_library(verbose: bool, ptxas_report: bool) -> None:
+    os.makedirs(OBJDIR, exist_ok=True)
     objs = []
     procs = []
     for src in sources():
-        obj = os.path.join(objdir, os.path.basename(src)[:-3] + ".o")
+        obj = os.path.join(OBJDIR, os.path.basename(src)[:-3] + ".o")
         cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
         if ptxas_report:
             cmd += ["-Xptxas", "-v"]
@@ -105,7 +147,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_report: bool = False
         print(" ".join(link), flush=True)
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

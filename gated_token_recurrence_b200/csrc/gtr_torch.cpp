@@ -267,4 +267,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gtr_torch", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__gtr_torch() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__gtr_torch() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", GTR_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
