@@ -38,7 +38,8 @@ EXPORTED = ("gtr_gla_fwd", "gtr_gla_fwd_f16", "gtr_gla_fwd_bf16", "gtr_gla_fwd_f
             "gtr_gla_workspace_bytes", "gtr_gla_fwd_ex", "gtr_gla_fwd_host",
             "gtr_gla_read_error", "gtr_gla_plan", "gtr_gla_workspace_init", "gtr_status_string",
             "gtr_version", "gtr_gla_fwd_noalloc", "gtr_gla_block_fwd", "gtr_sswiglu_dwconv",
-            "gtr_gla_workspace_debug", "gtr_ssm_conv", "gtr_ssm_scan", "gtr_ssm_step", "gtr_block_norm")
+            "gtr_gla_workspace_debug", "gtr_ssm_conv", "gtr_ssm_scan", "gtr_ssm_step", "gtr_block_norm",
+            "gtr_ssm_scan_plan")
 
 
 class GTRError(RuntimeError):
@@ -69,6 +70,7 @@ def _load() -> ctypes.CDLL:
     ssm = [vp, q, vp, q, vp, vp, q, vp, q, vp, q, vp, vp, i, vp, vp]
     lib.gtr_ssm_scan.argtypes = ssm + [vp, vp] + [i] * 8 + [vp]
     lib.gtr_ssm_step.argtypes = ssm + [vp] + [i] * 5 + [vp]
+    lib.gtr_ssm_scan_plan.argtypes = [i] * 8 + [ctypes.POINTER(i)]
     lib.gtr_block_norm.argtypes = [vp] * 5 + [i, i, vp, f, vp, vp, i, q, i, i, i, vp]
     lib.gtr_gla_workspace_debug.argtypes = [vp, i, ctypes.c_uint, vp]
     lib.gtr_gla_workspace_bytes.argtypes = [i] * 8
@@ -83,7 +85,7 @@ def _load() -> ctypes.CDLL:
                  "gtr_gla_fwd_ex", "gtr_gla_fwd_host", "gtr_gla_read_error", "gtr_gla_plan",
                  "gtr_gla_workspace_init", "gtr_version", "gtr_gla_fwd_noalloc", "gtr_gla_block_fwd",
                  "gtr_sswiglu_dwconv", "gtr_gla_workspace_debug", "gtr_ssm_conv", "gtr_ssm_scan",
-                 "gtr_ssm_step", "gtr_block_norm"):
+                 "gtr_ssm_step", "gtr_block_norm", "gtr_ssm_scan_plan"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -324,6 +326,16 @@ def ssm_scan(u, dt, A, Bm, Cm, grid: Tuple[int, int], direction: int = L2R, skip
     if st:
         raise GTRError(st, "gtr_ssm_scan")
     return out
+
+
+SSM_PLANS = ("walk", "deep4", "deep8", "deep8short", "wide32x8", "wide16x16", "wide16x8", "wide8x16", "wide8x8")
+
+
+def ssm_scan_plan(B: int, H: int, W: int, D: int, N: int, G: int = 1, dtype: int = F16, padded: bool = False) -> str:
+    """Name of the kernel that :func:`ssm_scan` takes for this problem; ``padded``: with lengths."""
+    plan_ = ctypes.c_int(0)
+    _check(lib.gtr_ssm_scan_plan(B, H, W, D, N, G, dtype, int(padded), ctypes.byref(plan_)), "gtr_ssm_scan_plan")
+    return SSM_PLANS[plan_.value]
 
 
 def ssm_step(u, dt, A, Bm, Cm, state, skip=None, z=None, dt_bias=None, softplus: bool = True, state_out=None,

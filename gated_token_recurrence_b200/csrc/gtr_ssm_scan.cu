@@ -654,6 +654,7 @@ struct ScanPlan {
   float fixed;              // share of that which does not grow with N
 };
 enum { kDeep4, kDeep8, kDeep8Short, kWide32x8, kWide16x16, kWide16x8, kWide8x16, kWide8x8, kPlans };
+static_assert(GTR_SSM_DEEP_4 == kDeep4 + 1 && GTR_SSM_WIDE_8X8 == kWide8x8 + 1, "the header's plans, in this order");
 constexpr ScanPlan kScanPlans[kPlans] = {
     {4, 128, 1, 28.f, 28.f, .36f},   {8, 128, 1, 36.f, 36.f, .36f},  {8, 64, 1, 41.f, 41.f, .48f},
     {8, 256, 3, 50.f, 86.f, .29f},   {16, 256, 2, 69.f, 91.f, .29f}, {16, 128, 3, 80.f, 139.f, .29f},
@@ -687,7 +688,7 @@ bool few_tokens(const SsmParams& p) {
 }
 
 template <typename T>
-gtr_status_t launch_scan_t(const SsmParams& p, cudaStream_t stream) {
+int choose_plan(const SsmParams& p) {
   const int smem[kPlans] = {DeepLayout<T, 16, 8, 1, 8>(p.N).total, DeepLayout<T, 16, 8, 2, 4>(p.N).total,
                             DeepLayout<T, 8, 8, 1, 8>(p.N).total,  WideLayout<T, 32, 8, 4>(p.N).total,
                             WideLayout<T, 16, 16, 4>(p.N).total,   WideLayout<T, 16, 8, 4>(p.N).total,
@@ -698,7 +699,12 @@ gtr_status_t launch_scan_t(const SsmParams& p, cudaStream_t stream) {
     const float c = plan_cost(p, i, smem[i]);
     if (c < least) best = i, least = c;
   }
-  switch (best) {
+  return best;
+}
+
+template <typename T>
+gtr_status_t launch_scan_t(const SsmParams& p, cudaStream_t stream) {
+  switch (choose_plan<T>(p)) {
     case kDeep4: return launch_deep<T, 16, 8, 1, 8, 8>(p, stream);
     case kDeep8: return launch_deep<T, 16, 8, 2, 4, 8>(p, stream);
     case kDeep8Short: return launch_deep<T, 8, 8, 1, 8, 8>(p, stream);
@@ -734,4 +740,25 @@ extern "C" gtr_status_t gtr_ssm_scan(const void* u, int64_t u_ld, const void* dt
     case GTR_BF16: return launch_scan_t<__nv_bfloat16>(p, s);
     default: return launch_scan_t<float>(p, s);
   }
+}
+
+extern "C" gtr_status_t gtr_ssm_scan_plan(int B, int grid_H, int grid_W, int D, int N, int G, int dtype, int padded,
+                                          int* plan) {
+  using namespace gtr;
+  const gtr_status_t st = validate_ssm_shape(B, grid_H, grid_W, D, N, G, dtype);
+  if (st != GTR_OK) return st;
+  if (!plan) return GTR_ERR_INVALID_ARG;
+  SsmParams p{};
+  p.B = B, p.L = grid_H * grid_W, p.D = D, p.N = N, p.G = G;
+  p.lengths = padded ? &p.B : nullptr;  // only whether there are any counts
+  if (few_tokens(p)) {
+    *plan = GTR_SSM_WALK;
+    return GTR_OK;
+  }
+  switch (dtype) {
+    case GTR_F16: *plan = 1 + choose_plan<__half>(p); break;
+    case GTR_BF16: *plan = 1 + choose_plan<__nv_bfloat16>(p); break;
+    default: *plan = 1 + choose_plan<float>(p);
+  }
+  return GTR_OK;
 }

@@ -236,11 +236,21 @@ gtr_status_t launch_ssm_walk(const SsmParams& p, int dtype, cudaStream_t stream)
   return launch_typed(p, dtype, true, stream);
 }
 
-gtr_status_t validate_ssm(const SsmParams& p, int grid_H, int grid_W, int direction, int dtype) {
-  if (!p.u || !p.dt || !p.A || !p.Bm || !p.Cm || !p.out || p.B <= 0 || grid_H <= 0 || grid_W <= 0 || p.D <= 0 ||
-      p.N <= 0 || p.G <= 0)
+gtr_status_t validate_ssm_shape(int B, int grid_H, int grid_W, int D, int N, int G, int dtype) {
+  if (B <= 0 || grid_H <= 0 || grid_W <= 0 || D <= 0 || N <= 0 || G <= 0 || dtype < GTR_F32 || dtype > GTR_BF16 ||
+      D % G != 0)
     return GTR_ERR_INVALID_ARG;
-  if (direction < GTR_L2R || direction > GTR_B2T || dtype < GTR_F32 || dtype > GTR_BF16) return GTR_ERR_INVALID_ARG;
+  const long long L = (long long)grid_H * grid_W;
+  if (N % 8 != 0 || N > 64 || (D / G) % 16 != 0 || D > (1 << 20) || B > 65535 || L > (1ll << 28))
+    return GTR_ERR_UNSUPPORTED;
+  return GTR_OK;
+}
+
+gtr_status_t validate_ssm(const SsmParams& p, int grid_H, int grid_W, int direction, int dtype) {
+  if (!p.u || !p.dt || !p.A || !p.Bm || !p.Cm || !p.out) return GTR_ERR_INVALID_ARG;
+  if (direction < GTR_L2R || direction > GTR_B2T) return GTR_ERR_INVALID_ARG;
+  const gtr_status_t shape = validate_ssm_shape(p.B, grid_H, grid_W, p.D, p.N, p.G, dtype);
+  if (shape == GTR_ERR_INVALID_ARG) return shape;
   for (const void* q : {p.u, p.dt, p.Bm, p.Cm, p.z, (const void*)p.A, (const void*)p.state_in,
                         (const void*)p.state_out, (const void*)p.out})
     if (!aligned_to(q, 16)) return GTR_ERR_INVALID_ARG;
@@ -250,11 +260,8 @@ gtr_status_t validate_ssm(const SsmParams& p, int grid_H, int grid_W, int direct
   if (p.u_ld < p.D || p.dt_ld < p.D || p.bm_ld < gn || p.cm_ld < gn || (p.z && p.z_ld < p.D)) return GTR_ERR_INVALID_ARG;
   for (long long ld : {p.u_ld, p.dt_ld, p.bm_ld, p.cm_ld, p.z ? p.z_ld : 0ll})
     if (ld % (16 / es) != 0) return GTR_ERR_INVALID_ARG;
-  if (p.D % p.G != 0) return GTR_ERR_INVALID_ARG;
-  const long long L = (long long)grid_H * grid_W;
-  if (p.N % 8 != 0 || p.N > 64 || (p.D / p.G) % 16 != 0 || p.D > (1 << 20) || p.B > 65535 || L > (1ll << 28))
-    return GTR_ERR_UNSUPPORTED;
-  const long long rows = p.B * L;
+  if (shape != GTR_OK) return shape;
+  const long long rows = (long long)p.B * grid_H * grid_W;
   for (long long ld : {p.u_ld, p.dt_ld, p.bm_ld, p.cm_ld, p.z ? p.z_ld : 0ll})
     if (ld > (1ll << 32) || (double)rows * (double)ld >= 1e12) return GTR_ERR_UNSUPPORTED;
   const size_t no = span_bytes(rows, p.D, p.D, es), ns = (size_t)p.B * p.D * p.N * 4, na = (size_t)p.D * p.N * 4;

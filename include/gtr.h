@@ -355,6 +355,26 @@ gtr_status_t gtr_ssm_step(const void *u, int64_t u_ld, const void *dt, int64_t d
                           int D, int N, int G, int dtype, gtr_stream_t stream);
 
 /*
+ * The kernel that gtr_ssm_scan takes for a problem (`padded`: with `lengths`), written to *plan:
+ * token by token in registers; one block an SM over tiles of 4 or 8 channels ("deep", the last
+ * with shorter tiles); blocks of TL x TS positions a warp ("wide").  Host-only; what is refused is
+ * what gtr_ssm_scan refuses for these sizes.
+ */
+enum {
+  GTR_SSM_WALK = 0,
+  GTR_SSM_DEEP_4 = 1,
+  GTR_SSM_DEEP_8 = 2,
+  GTR_SSM_DEEP_8_SHORT = 3,
+  GTR_SSM_WIDE_32X8 = 4,
+  GTR_SSM_WIDE_16X16 = 5,
+  GTR_SSM_WIDE_16X8 = 6,
+  GTR_SSM_WIDE_8X16 = 7,
+  GTR_SSM_WIDE_8X8 = 8
+};
+gtr_status_t gtr_ssm_scan_plan(int B, int grid_H, int grid_W, int D, int N, int G, int dtype,
+                               int padded, int *plan);
+
+/*
  * The norms after one block and before the next, fused with the block's gate, its residual
  * scale and the residual stream.  Per token row (C channels), y the block's output and h the
  * residual stream:
