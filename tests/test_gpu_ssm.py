@@ -471,3 +471,57 @@ def test_a_refused_launch_leaves_no_error_behind():
                     refused = e.status == 3
         assert refused
         assert torch.equal(split(), ref)
+
+
+# ----------------------------------------------------------------------------------- long memories
+TILES = {"deep4": (16, 8), "deep8": (16, 8), "deep8short": (8, 8), "wide32x8": (32, 8), "wide16x16": (16, 16),
+         "wide16x8": (16, 8), "wide8x16": (8, 16), "wide8x8": (8, 8)}  # time lanes, positions a lane
+
+
+def long_memory(B, L, D, N, delta):
+    """Constant steps and no input: h = h0 exp(L delta A), and every exponential repeats its error."""
+    c = scan_case("f32", B, 1, L, D, N, 1, skip=False, z=False, bias=False, softplus=False)
+    c["dt"][:], c["u"][:] = delta, 0.0
+    arg = L * float(torch.tensor(delta)) * c["A"].double().numpy()
+    return c, c["state"].double().numpy() * np.exp(arg), np.abs(arg)
+
+
+@pytest.mark.parametrize("delta", [1e-6, 1e-5, 1e-4])
+@pytest.mark.parametrize("B,D,N", [(1, 48, 16), (1, 768, 16), (1, 1200, 16), (3, 1584, 16), (5, 1440, 8), (9, 1056, 8)])
+def test_long_memory_of_the_scan(B, D, N, delta):
+    """Per tile of TL TS positions a state meets TL - 1 lane products and TS decays, each an
+    exponential (2^-22.5) and two roundings of fp32, besides 2^-19 of its argument: far fewer than
+    one a position (16,384 at the 1e-7 that was measured for each would exceed the bound)."""
+    L = 128 * 128
+    TL, TS = TILES[gtr.ssm_scan_plan(B, 1, L, D, N, 1, gtr.F32)]
+    c, ref, arg = long_memory(B, L, D, N, delta)
+    g = on_gpu(c)
+    so = torch.empty_like(g["state"])
+    gtr.ssm_scan(**g, grid=(1, L), softplus=False, state_out=so)
+    factors = -(-L // (TL * TS)) * (TL - 1 + TS)
+    assert (np.abs(f64(so) - ref) <= (factors * (2.0 ** -22.5 + 2 * 2.0 ** -24) + 2.0 ** -19 * arg) * np.abs(ref)).all()
+
+
+@pytest.mark.parametrize("delta", [1e-6, 1e-4])
+def test_long_memory_of_the_step(delta):
+    """One exponential and one rounding a token."""
+    T = 4096
+    c, ref, arg = long_memory(2, T, 96, 16, delta)
+    g = on_gpu(c)
+    one = {k: g[k][:, 0] for k in ("u", "dt", "Bm", "Cm")}
+    for _ in range(T):
+        gtr.ssm_step(**one, A=g["A"], state=g["state"], softplus=False)
+    assert (np.abs(f64(g["state"]) - ref) <= (T * (2.0 ** -22.5 + 2.0 ** -24) + 2.0 ** -19 * arg) * np.abs(ref)).all()
+
+
+def test_scan_outputs_of_large_steps():
+    """softplus is the identity at 60, exp(-60) is gone in fp32; with open gates the outputs say so."""
+    B, L, D, N = 1, 40, 32, 16
+    c = scan_case("f32", B, 1, L, D, N, 1)
+    c["dt"][:] = 60.0
+    ref, st, oerr, serr = oracle.ssm_scan(**c, H=1, W=L, rounding=ROUNDING)
+    so = torch.empty(B, D, N, device="cuda")
+    out = gtr.ssm_scan(**on_gpu(c), grid=(1, L), state_out=so)
+    within(out, ref, oerr + half_step("f32", ref), "out")
+    within(so, st, serr + half_step("f32", st), "state")
+    assert np.abs(ref).max() > 100.0
