@@ -13,8 +13,9 @@
 // loads in flight is the number of resident rows, so a thread holds little: requesting the
 // weights of the second half early, or walking over rows with weights and the next row in
 // registers, measured 20 to 60% slower on large inputs.  Measured: 30,720 rows of 1536, bf16
-// with fp32 residual, 98 us, 88% of the measured HBM bandwidth; 1600 rows of 384, fp16, 3.0 us;
-// 2441 rows of 8192, bf16 with a gate for each token, 51 us, 60%.
+// with fp32 residual, 98 us, 88% of the measured HBM bandwidth; 1600 rows of 384, fp16, 3.0 us.
+// Rows above 4096 leave one or two blocks on an SM, whose loads, sums and stores follow one
+// another: bf16 with a gate for each token, 2441 rows of 8192 51 us, 60%; 1220 of 16384 78 us, 39%.
 #include "gtr_common.cuh"
 #include "gtr_launch.cuh"
 #include "gtr_math.cuh"
@@ -156,10 +157,11 @@ gtr_status_t launch_norm(const NormParams& p, cudaStream_t stream) {
   return launch_serial(block_norm_kernel<T, R, TPR, NV>, dim3((unsigned)grid), dim3(TPR == 32 ? 128 : TPR), 0, stream, p);
 }
 
-// TPR by the row's pieces.  Up to 64 pieces a warp holds two a thread (54,000 rows of 384: 47 us,
-// with 64 threads and one piece 58 us), except where the rows are few and two warps a row are
-// quicker (1600 rows: 4.4 and 3.6 us); up to 256 pieces one a thread (30,720 rows of 192 pieces:
-// 98 us, two a thread 106 us); above, two: a block of half the threads waits less at its barriers.
+// TPR by the row's pieces.  Up to 64 pieces a warp holds two a thread, except where the rows are
+// few: two warps a row with one piece a thread are quicker (1600 rows of 384, fp16: 2.95 us, a
+// warp 3.44 us).  They are for many rows as well (54,000 rows, bf16: 43 us, a warp 47 us), which
+// this rule does not use.  Up to 256 pieces one a thread (30,720 rows of 192 pieces: 98 us, two a
+// thread 100 us); above, two: a block of half the threads waits less at its barriers.
 template <typename T, typename R>
 gtr_status_t launch_norm_c(const NormParams& p, cudaStream_t stream) {
   const int nvec = p.C / Vec8<T>::N;

@@ -11,9 +11,11 @@
 // whatever the direction: the direction only changes which row comes next.
 //
 // Bound: HBM, 2 elements of traffic for 2 K + 5 operations.  Measured (bf16, K = 4, SiLU): eight
-// 48 x 80 grids of 1152 channels 33 us, 65% of the measured HBM bandwidth (without SiLU's two
-// special functions per element 30 us); one 40 x 40 grid of 768 channels 4.0 us.  It was 54 and
-// 12 us with taps read from global memory by each thread and strips of 8 and 4 positions.
+// 48 x 80 grids of 1152 channels 32 us, 67% of the measured HBM bandwidth (K = 2 29 us, 76%; fp32
+// 48 us, 90%); one 128 x 128 grid of 768 channels 16 us, 48% (fp32 21 us, 75%): a few blocks more
+// than a wave, see launch_conv; one 40 x 40 grid of 768 channels 3.9 us.  It was 54 us on the first
+// and 12 us on the last with taps read from global memory by each thread and strips of 8 and 4
+// positions.
 #include "gtr_common.cuh"
 #include "gtr_launch.cuh"
 #include "gtr_math.cuh"
@@ -178,10 +180,13 @@ __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(const ConvParams
 template <typename T, int K>
 gtr_status_t launch_conv(ConvParams p, int B, cudaStream_t stream) {
   p.nvec = (unsigned)(p.C / Vec8<T>::N);
-  // A strip is as long as one wave of threads (four blocks an SM) allows, 4 to 24 positions: a
-  // shorter one pays its taps and its K - 1 rows too often (eight 48 x 80 grids of 1152
-  // channels, bf16: 4 positions 53 us, 24 33 us), a longer one leaves SMs idle (one 40 x 40
-  // grid of 768 channels: 4.6 and 9.0 us).
+  // A strip is about as long as makes one wave of four blocks an SM, 4 to 24 positions: a shorter
+  // one pays its taps and its K - 1 rows too often (eight 48 x 80 grids of 1152 channels, bf16: 4
+  // positions 51 us, 24 32 us), a longer one leaves SMs idle (one 40 x 40 grid of 768 channels: 4
+  // positions 4.0 us, 24 6.4 us).  Four blocks is what 16-bit data and K = 3 or 4 hold (102 and 124
+  // registers); the other kernels hold six to eight.  The share is cut to whole positions first,
+  // so a launch may have a few blocks more than the wave (one 128 x 128 grid of 768 channels: 615
+  // for 592, 16.0 us; strips of 28 13.6 us).
   const long long fair = (long long)B * p.L * p.nvec / (4ll * 148 * kConvThreads);
   p.strip = p.L == 1 ? 1 : (int)(fair < 4 ? 4 : fair > 24 ? 24 : (fair + 3) / 4 * 4);
   p.strips = (unsigned)((p.L + p.strip - 1) / p.strip);

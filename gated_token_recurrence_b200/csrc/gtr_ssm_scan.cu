@@ -646,9 +646,15 @@ gtr_status_t launch_deep(const SsmParams& p, cudaStream_t stream) {
 //   W = 432  wide<32, 8> 86, wide<16, 16> 91;    W = 576  wide<16, 16> 92, wide<16, 8> 106
 //   W = 880  wide<16, 8> 139, wide<16, 16> 154;  W = 1152 wide<8, 16> 164, wide<16, 16> 182
 //   W = 1728 wide<8, 8> 247, wide<8, 16> 268
+// Other types and N take the same figures; against every other plan on 16 shapes of fp32 and of N =
+// 8, 32 and 64 the choice was the quickest but for two fp32 ones (two sequences of 4096 positions
+// and 1536 channels: deep<8> 237 us, wide<16, 8> 224 us; four of 2048 and 864: 124 and 114 us).
 // The lengths of a padded batch are on the device; its blocks are counted half, as if the
 // lengths were spread evenly (three sequences of 416 channels, one full, one of some tokens, one
-// empty: deep 27 us, a plan for all of them at once 56 us).
+// empty: deep 27 us, a plan for all of them at once 56 us).  A batch that comes with lengths and
+// is full pays for that: with and without them eight sequences of 1600 positions and 768 channels
+// 147 and 112 us, four of 4096 and 1536 335 and 272 us, four of 1600 and 768 89 and 76 us, eight of
+// 3840 and 1536 498 and 453 us.
 struct ScanPlan {
   int channels, positions;  // of a block's tile
   int holds;                // blocks on an SM where shared memory allows it
@@ -666,7 +672,7 @@ constexpr ScanPlan kScanPlans[kPlans] = {
 float plan_cost(const SsmParams& p, int plan, int smem) {
   constexpr float kNever = 3e38f;
   const ScanPlan& s = kScanPlans[plan];
-  const int fits = (kMaxSmem + 1024) / (smem + 1024);  
+  const int fits = (kMaxSmem + 1024) / (smem + 1024);
   if (smem > kMaxSmem || p.D / p.G % s.channels != 0) return kNever;
   const int holds = fits < s.holds ? fits : s.holds;
   const auto wave = [&](long long blocks) {  // microseconds with so many blocks on an SM
@@ -680,10 +686,12 @@ float plan_cost(const SsmParams& p, int plan, int smem) {
 }
 
 // Prompts that leave a tile mostly empty walk token by token instead (gtr_ssm_step.cu).  Measured
-// (bf16, N = 16, 1536 channels), walk and tiles: 512 sequences of 4 tokens 77 and 500 us, of 24
-// 376 and 505 us; 16 sequences of 4 tokens 4.3 and 19.9 us, of 12 10.1 and 20.0 us; 4 sequences of
-// 4 tokens 3.8 and 8.4 us, of 12 8.9 and 8.4 us; one sequence of 4 tokens, 768 channels: 3.6 and
-// 3.5 us.
+// (1536 channels), walk and the quickest tiles: bf16, N = 16, 512 sequences of 24 tokens 377 and 514
+// us, of 32 496 and 516 us; 16 sequences of 24 17 and 21 us, of 32 26 and 21 us; 4 sequences of 8
+// 5.2 and 8.3 us, of 12 7.2 and 8.4 us, of 16 9.3 and 8.4 us.  fp32: 512 of 24 341 and 543 us, 16 of
+// 24 20 and 23 us, 4 of 8 3.9 and 8.8 us.  The tiles grow faster with N than the walk: N = 64, bf16,
+// 512 of 24 698 and 2153 us, of 32 918 and 2163 us; 16 of 32 45 and 81 us; 4 of 12 9.0 and 27 us,
+// past the border of this rule, which looks at lengths and channels alone.
 bool few_tokens(const SsmParams& p) {
   const long long channels = (long long)p.B * p.D;
   return channels >= 16384 ? p.L <= 24 : channels >= 4096 && p.L <= 8;

@@ -7,7 +7,9 @@
 // leaves sequence j's in lane j, for the skip term and the gate.
 //
 // Bound: HBM, the states' 8 N bytes per channel in and out against 8 bytes (16-bit data) of u,
-// dt, z and out.
+// dt, z and out.  Measured (1536 channels): 512 sequences of N = 16, bf16 23.6 us, 69% of the
+// measured HBM bandwidth, fp32 25.3 us, 68%; 64 of N = 64, bf16 11.0 us, 71%, fp32 12.2 us, 65%.
+// There the loads' latency is left: a thread asks for all it needs once.
 #include "gtr_launch.cuh"
 #include "gtr_ssm.cuh"
 #include "gtr_ssm_host.h"
@@ -188,9 +190,9 @@ template <typename T, int LPC, int NV>
 gtr_status_t launch_step_v(const SsmParams& p, cudaStream_t stream) {
   constexpr int kCh = kStepThreads / LPC;
   const unsigned gx = (unsigned)((p.D + kCh - 1) / kCh);
-  // LPC sequences a thread where they fill the GPU and the registers hold their states (bf16, D =
-  // 1536: N = 16, 512 sequences 25 against 30 us, 4 sequences of D = 768 2.7 against 2.0 us; N =
-  // 64, 64 sequences 18 against 13.5 us)
+  // LPC sequences a thread where they fill the GPU and the registers hold their states (bf16, LPC
+  // and one, D = 1536: N = 16, 512 sequences 23.5 and 27.4 us, 64 4.3 and 4.8 us, 43 3.5 and 3.5
+  // us; 4 sequences of D = 768 2.4 and 1.9 us; N = 64, 64 sequences 15.1 and 11.0 us)
   if constexpr (NV == 1) {
     if ((long long)p.B * p.D >= 64 * 1024)
       return launch_serial(ssm_step_kernel<T, LPC, NV, LPC>, dim3(gx, (unsigned)((p.B + LPC - 1) / LPC)),

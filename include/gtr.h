@@ -292,7 +292,8 @@ gtr_status_t gtr_sswiglu_dwconv(const void *xg, const void *xv, const float *con
  *     input may be a column range of a wider projection.  Outputs are contiguous;
  *   - no output may overlap an input or another output, except where an argument says that
  *     it may be the same buffer (GTR_ERR_INVALID_ARG);
- *   - sums, states and norms are held in fp32; each output is rounded once;
+ *   - sums, states and norms are held in fp32; each output is rounded once.  A sigmoid below 2^-126
+ *     (SiLU of arguments below -87.3) counts as 0;
  *   - `direction` is the scan order of gtr_gla_fwd over grid_H x grid_W tokens per sequence.
  *     A plain sequence of L tokens is the grid 1 x L in direction GTR_L2R;
  *   - `lengths` [B] int32 (or NULL: all full) gives the number of tokens that each sequence of
@@ -333,8 +334,9 @@ gtr_status_t gtr_ssm_conv(const void *x, int64_t x_ld, const float *w, const flo
  *     a rate of -inf forgets at every step above 0);  skip, dt_bias [D] fp32 or NULL (0)
  *   state_in [B, D, N] fp32: h before the first position (NULL: zeros);  state_out: h after
  *     the last (NULL: not wanted; may be state_in)
- *   N a multiple of 8 up to 64;  D / G a multiple of 16;  B <= 65535; otherwise
- *   GTR_ERR_UNSUPPORTED.
+ *   N a multiple of 8 up to 64 (a token's Bm and Cm are read in pieces of 16 bytes; a model of
+ *     fewer states is served by more, with Bm, Cm and A of 0);  D / G a multiple of 16;
+ *     B <= 65535; otherwise GTR_ERR_UNSUPPORTED.
  */
 gtr_status_t gtr_ssm_scan(const void *u, int64_t u_ld, const void *dt, int64_t dt_ld, const float *A,
                           const void *Bm, int64_t bm_ld, const void *Cm, int64_t cm_ld,
@@ -386,7 +388,8 @@ gtr_status_t gtr_ssm_scan_plan(int B, int grid_H, int grid_W, int D, int N, int 
  *   gate in `dtype`: [B, C] (one row per sequence) or, with gate_per_token, [B, L, C]; act =
  *     SiLU where gate_silu is not 0, else the identity
  *   post_w, pre_w, scale [C] fp32;  pre_w and n_out are both given or both NULL
- *   eps >= 0 (finite);  C a multiple of 8 up to 16384 (16-bit data) or of 4 up to 8192 (fp32),
+ *   eps >= 0 (finite); a row whose sum of squares leaves fp32's range has no norm (values above
+ *     some 1e19 give 0; with eps = 0, values all below some 1e-23 give infinities);  C a multiple of 8 up to 16384 (16-bit data) or of 4 up to 8192 (fp32),
  *     otherwise GTR_ERR_UNSUPPORTED.
  */
 gtr_status_t gtr_block_norm(const void *y, const void *h, const float *post_w, const float *pre_w,

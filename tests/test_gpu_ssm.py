@@ -525,3 +525,18 @@ def test_scan_outputs_of_large_steps():
     within(out, ref, oerr + half_step("f32", ref), "out")
     within(so, st, serr + half_step("f32", st), "state")
     assert np.abs(ref).max() > 100.0
+
+
+@pytest.mark.parametrize("B,D,L,N", [(1, 48, 137, 1), (16, 1024, 8, 4)])
+def test_fewer_states_are_served_by_eight(B, D, L, N):
+    """Bm, Cm and A of 0 behind the model's own states, as the header says."""
+    c = scan_case("bf16", B, 1, L, D, N, 1)
+    ref, st, oerr, serr = oracle.ssm_scan(**c, H=1, W=L, rounding=ROUNDING)
+    pad = lambda t: torch.nn.functional.pad(t, (0, 8 - N))
+    c.update({k: pad(c[k]) for k in ("A", "Bm", "Cm", "state")})
+    so = torch.empty(B, D, 8, device="cuda")
+    out = gtr.ssm_scan(**on_gpu(c), grid=(1, L), state_out=so)
+    # the added terms are zeros: adding them rounds nothing
+    within(out, ref, oerr + half_step("bf16", ref), "out")
+    within(so[..., :N].contiguous(), st, serr + half_step("f32", st), "state")
+    assert (so[..., N:] == 0).all()
