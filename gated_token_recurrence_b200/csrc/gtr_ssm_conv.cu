@@ -13,7 +13,7 @@
 // Bound: HBM, 2 elements of traffic for 2 K + 5 operations.  Measured (bf16, K = 4, SiLU): eight
 // 48 x 80 grids of 1152 channels 32 us, 67% of the measured HBM bandwidth (K = 2 29 us, 76%; fp32
 // 48 us, 90%); one 128 x 128 grid of 768 channels 16 us, 48% (fp32 21 us, 75%): a few blocks more
-// than a wave, see launch_conv; one 40 x 40 grid of 768 channels 3.9 us.  It was 54 us on the first
+// than a wave, see launch_conv; one 40 x 40 grid of 768 channels 4.0 us.  It was 54 us on the first
 // and 12 us on the last with taps read from global memory by each thread and strips of 8 and 4
 // positions.
 #include "gtr_common.cuh"

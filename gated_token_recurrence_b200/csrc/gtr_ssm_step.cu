@@ -191,7 +191,7 @@ gtr_status_t launch_step_v(const SsmParams& p, cudaStream_t stream) {
   constexpr int kCh = kStepThreads / LPC;
   const unsigned gx = (unsigned)((p.D + kCh - 1) / kCh);
   // LPC sequences a thread where they fill the GPU and the registers hold their states (bf16, LPC
-  // and one, D = 1536: N = 16, 512 sequences 23.5 and 27.4 us, 64 4.3 and 4.8 us, 43 3.5 and 3.5
+  // and one, D = 1536: N = 16, 512 sequences 23.6 and 27.4 us, 64 4.3 and 4.8 us, 43 3.5 and 3.5
   // us; 4 sequences of D = 768 2.4 and 1.9 us; N = 64, 64 sequences 15.1 and 11.0 us)
   if constexpr (NV == 1) {
     if ((long long)p.B * p.D >= 64 * 1024)
